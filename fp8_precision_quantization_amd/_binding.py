@@ -66,8 +66,9 @@ def lib():
                 raise RuntimeError(
                     "libmxcast.so is missing at %s; build it with "
                     "`python -m fp8_precision_quantization_amd.build`" % LIB_PATH)
+            from ._train import SIGNATURES as train_signatures
             handle = ctypes.CDLL(LIB_PATH)
-            for name, (args, res) in SIGNATURES.items():
+            for name, (args, res) in {**SIGNATURES, **train_signatures}.items():
                 f = getattr(handle, name)
                 f.argtypes = args
                 f.restype = res

@@ -1,0 +1,509 @@
+// MoE router: expert choice, gates, per-expert counts and the balance loss;
+// and the gradient of the logits.
+//
+//   p = softmax(z); chosen = the topk largest logits; gates = p[chosen]
+//   (divided by their sum); counts, group ends; balance[e] = E counts[e] /
+//   (topk N^2); loss = sum_e balance[e] sum_rows p[e].
+//   dz[e] = p[e] (dp[e] - sum_i p[i] dp[i]),
+//   dp[e] = dloss balance[e] + sum_j [chosen_j = e] d_j.
+//
+// A row belongs to G lanes: 16 (four rows to a wave) up to 256 experts, the
+// wave for more.  A lane holds V logits, in pieces of U consecutive columns
+// (U a 16-byte load where alignment allows, else 1); piece p of a row sits in
+// lane p % G.  The row is read once: maximum, exponentials, their sum and the
+// topk selections all work on registers and on lane moves.
+//
+// Selection: logits become integers that order like them (NaN above +inf, a
+// closed expert 0); each round takes the maximum over the group, then the
+// lowest column that has it, and clears that element.
+//
+// Sums over rows (p for the loss) stay in a lane's registers over all its
+// rows, meet in LDS, and leave as one row of partial sums per workgroup; the
+// last step adds these up in a fixed order.  Counts are integers: LDS atomics
+// in any order give the same result.
+#include "mx_train.h"
+#include "mx_train_launch.h"
+#include "mxtrain.h"
+
+namespace mx {
+
+constexpr int kRouterThreads = 1024;
+constexpr int kRouterWaves = kRouterThreads / 64;
+constexpr int64_t kRouterBlocks = 256;   // one workgroup to a CU
+
+struct RouterArgs {
+  const void* z;
+  int64_t ld, rows;
+  const uint8_t* valid;
+  int32_t experts, topk, normalize, align;
+  int32_t *chosen, *counts, *ends;
+  float *gates, *lse, *balance, *loss;
+  // workspace: per workgroup a row of p sums, then a row of counts, then the
+  // number of rows that took part
+  float* part_p;
+  int32_t* part_n;
+  int32_t* part_rows;
+  // backward
+  const int32_t* in_chosen;
+  const float *in_lse, *in_gates, *in_balance, *dgates, *dloss;
+  void* dz;
+};
+
+template <int G, int U>
+__device__ __forceinline__ int router_col(int v, int gl) {
+  return ((v / U) * G + gl) * U + v % U;
+}
+
+// This lane's logits of a row as binary32; columns past the end give `pad`.
+template <typename T, int G, int V, int U>
+__device__ __forceinline__ void load_logits(const T* row, int experts, int gl, float pad, float (&z)[V]) {
+#pragma unroll
+  for (int p = 0; p < V / U; ++p) {
+    const int c = router_col<G, U>(p * U, gl);
+    float f[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i)
+      f[i] = pad;
+    if (c < experts)
+      unpack(row + c, f);
+#pragma unroll
+    for (int i = 0; i < U; ++i)
+      z[p * U + i] = f[i];
+  }
+}
+
+// Integer that orders like the logit: NaN highest, -inf (a closed expert) 0.
+// Adding +0 turns -0 into +0, which it equals.
+__device__ __forceinline__ uint32_t order_key(float z) {
+  if (z != z)
+    return 0xFFFFFFFFu;
+  const uint32_t u = __float_as_uint(z + 0.0f);
+  const uint32_t k = (u & 0x80000000u) ? ~u : u | 0x80000000u;
+  return k == 0x007FFFFFu ? 0u : k;
+}
+__device__ __forceinline__ float key_value(uint32_t k) {
+  if (k == 0xFFFFFFFFu)
+    return __uint_as_float(0x7FC00000u);
+  return __uint_as_float((k & 0x80000000u) ? k & 0x7FFFFFFFu : ~k);
+}
+
+// counts, ends, balance and loss from totals in LDS (tot_p, tot_n) and the
+// number of rows; by wave 0.
+__device__ __forceinline__ void router_finish(const RouterArgs& a, const float* tot_p, const int32_t* tot_n,
+                                              int32_t n_rows) {
+  const int lane = threadIdx.x & 63;
+  int32_t before = 0;
+  float loss = 0.0f;
+  const float n = (float)n_rows;
+  for (int e0 = 0; e0 < a.experts; e0 += 64) {
+    const int e = e0 + lane;
+    const bool on = e < a.experts;
+    const int32_t c = on ? tot_n[e] : 0;
+    int32_t sum = (c + a.align - 1) / a.align * a.align;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int32_t o = __shfl_up(sum, d);
+      if (lane >= d)
+        sum += o;
+    }
+    const float bal = n_rows > 0 ? (float)a.experts * (float)c / ((float)a.topk * n * n) : 0.0f;
+    if (on) {
+      a.counts[e] = c;
+      a.ends[e] = before + sum;
+      a.balance[e] = bal;
+      if (n_rows > 0)
+        loss += bal * tot_p[e];
+    }
+    before += __shfl(sum, 63);
+  }
+  loss = lanes_sum(loss);
+  if (lane == 0)
+    *a.loss = loss;
+}
+
+template <typename T, int G, int V, int U>
+__global__ __launch_bounds__(kRouterThreads) void router_fwd_kernel(RouterArgs a) {
+  constexpr int kRows = 64 / G;   // rows to a wave
+  __shared__ float tot_p[MX_MAX_GROUPS];
+  __shared__ int32_t tot_n[MX_MAX_GROUPS];
+  __shared__ int32_t tot_rows;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63;
+  const int gl = lane % G;
+  for (int e = threadIdx.x; e < a.experts; e += kRouterThreads) {
+    tot_p[e] = 0.0f;
+    tot_n[e] = 0;
+  }
+  if (threadIdx.x == 0)
+    tot_rows = 0;
+  lds_barrier();
+
+  float psum[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+    psum[v] = 0.0f;
+  int32_t rows_here = 0;
+
+  const int64_t stride = (int64_t)gridDim.x * kRouterWaves * kRows;
+  for (int64_t base = ((int64_t)blockIdx.x * kRouterWaves + wave) * kRows; base < a.rows; base += stride) {
+    const int64_t row = base + lane / G;
+    const bool in = row < a.rows && (a.valid == nullptr || a.valid[row] != 0);
+    float z[V];
+    load_logits<T, G, V, U>(static_cast<const T*>(a.z) + (in ? row : 0) * a.ld, in ? a.experts : 0, gl, -INFINITY, z);
+    uint32_t key[V];
+    uint32_t top = 0;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      key[v] = order_key(z[v]);
+      top = max(top, key[v]);
+    }
+    top = lanes_max<G>(top);
+    const bool part = top != 0;   // the row takes part
+    const float zmax = part ? key_value(top) : 0.0f;
+    float e[V], sum = 0.0f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      e[v] = exp_fast(z[v] - zmax);
+      sum += e[v];
+    }
+    sum = lanes_sum<G>(sum);
+    const float inv = part ? 1.0f / sum : 0.0f;
+    if (part) {
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        psum[v] += e[v] * inv;
+    }
+    rows_here += part && gl == 0;
+
+    // lane j of the group keeps the choices j, j + G, ...
+    constexpr int kKeep = (MX_MAX_TOPK + G - 1) / G;
+    int32_t idx[kKeep];
+    float gate[kKeep];
+#pragma unroll
+    for (int i = 0; i < kKeep; ++i) {
+      idx[i] = -1;
+      gate[i] = 0.0f;
+    }
+    for (int j = 0; j < a.topk; ++j) {
+      uint32_t best = 0;
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        best = max(best, key[v]);
+      best = lanes_max<G>(best);
+      uint32_t col = 0xFFFFFFFFu;
+#pragma unroll
+      for (int v = V - 1; v >= 0; --v)
+        col = key[v] == best ? (uint32_t)router_col<G, U>(v, gl) : col;
+      col = lanes_min<G>(col);
+      const bool found = best != 0;
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        key[v] = (uint32_t)router_col<G, U>(v, gl) == col ? 0u : key[v];
+      if (found && gl == j % G) {
+        const float p = exp_fast(key_value(best) - zmax) * inv;
+#pragma unroll
+        for (int i = 0; i < kKeep; ++i)
+          if (i == j / G) {
+            idx[i] = (int32_t)col;
+            gate[i] = p;
+          }
+        atomicAdd(&tot_n[col], 1);
+      }
+    }
+    if (a.normalize) {
+      float total = 0.0f;
+#pragma unroll
+      for (int i = 0; i < kKeep; ++i)
+        total += gate[i];
+      total = lanes_sum<G>(total);
+#pragma unroll
+      for (int i = 0; i < kKeep; ++i)
+        gate[i] = part ? gate[i] / total : 0.0f;
+    }
+    if (row < a.rows) {
+#pragma unroll
+      for (int i = 0; i < kKeep; ++i) {
+        const int j = i * G + gl;
+        if (j < a.topk) {
+          a.chosen[row * a.topk + j] = idx[i];
+          a.gates[row * a.topk + j] = idx[i] < 0 ? 0.0f : gate[i];
+        }
+      }
+      if (gl == 0)
+        a.lse[row] = part ? zmax + logf(sum) : 0.0f;
+    }
+  }
+
+  // p sums: the groups of a wave by lane moves, the waves one after another
+  // through LDS
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    if constexpr (G == 16) {
+      const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(psum[v]), __float_as_uint(psum[v]), false, false);
+      psum[v] = __uint_as_float(s[0]) + __uint_as_float(s[1]);
+      const auto t = __builtin_amdgcn_permlane32_swap(__float_as_uint(psum[v]), __float_as_uint(psum[v]), false, false);
+      psum[v] = __uint_as_float(t[0]) + __uint_as_float(t[1]);
+    }
+  }
+  atomicAdd(&tot_rows, rows_here);
+  for (int w = 0; w < kRouterWaves; ++w) {
+    if (wave == w && lane < G) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const int c = router_col<G, U>(v, gl);
+        if (c < a.experts)
+          tot_p[c] += psum[v];
+      }
+    }
+    lds_barrier();
+  }
+  if (gridDim.x == 1) {
+    if (wave == 0)
+      router_finish(a, tot_p, tot_n, tot_rows);
+    return;
+  }
+  for (int c = threadIdx.x; c < a.experts; c += kRouterThreads) {
+    a.part_p[(int64_t)blockIdx.x * a.experts + c] = tot_p[c];
+    a.part_n[(int64_t)blockIdx.x * a.experts + c] = tot_n[c];
+  }
+  if (threadIdx.x == 0)
+    a.part_rows[blockIdx.x] = tot_rows;
+}
+
+// Adds up the workgroups' rows: a column belongs to 1024 / ceil2(experts)
+// threads, each taking every so many-th row.
+__global__ __launch_bounds__(kRouterThreads) void router_fold_kernel(RouterArgs a, int32_t blocks) {
+  __shared__ float sum_p[kRouterThreads];
+  __shared__ int32_t sum_n[kRouterThreads];
+  __shared__ int32_t rows_total;
+  if (threadIdx.x == 0)
+    rows_total = 0;
+  lds_barrier();
+  int width = 16;
+  while (width < a.experts)
+    width *= 2;
+  const int slices = kRouterThreads / width;
+  const int c = threadIdx.x % width, slice = threadIdx.x / width;
+  float p = 0.0f;
+  int32_t n = 0;
+  if (c < a.experts) {
+#pragma unroll 4
+    for (int b = slice; b < blocks; b += slices) {
+      p += a.part_p[(int64_t)b * a.experts + c];
+      n += a.part_n[(int64_t)b * a.experts + c];
+    }
+  }
+  sum_p[threadIdx.x] = p;
+  sum_n[threadIdx.x] = n;
+  if ((int)threadIdx.x < blocks)
+    atomicAdd(&rows_total, a.part_rows[threadIdx.x]);
+  lds_barrier();
+  if (slice == 0) {
+    for (int s = 1; s < slices; ++s) {
+      p += sum_p[s * width + c];
+      n += sum_n[s * width + c];
+    }
+    sum_p[c] = p;
+    sum_n[c] = n;
+  }
+  lds_barrier();
+  if (threadIdx.x < 64)
+    router_finish(a, sum_p, sum_n, rows_total);
+}
+
+constexpr int kRouterBwdThreads = 256;
+
+template <typename T, int G, int V, int U>
+__global__ __launch_bounds__(kRouterBwdThreads) void router_bwd_kernel(RouterArgs a) {
+  constexpr int kRows = 64 / G;
+  constexpr int kWaves = kRouterBwdThreads / 64;
+  constexpr int kKeep = (MX_MAX_TOPK + G - 1) / G;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63;
+  const int gl = lane % G;
+  const float dloss = a.dloss != nullptr ? *a.dloss : 0.0f;
+  float bal[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int c = router_col<G, U>(v, gl);
+    bal[v] = c < a.experts ? dloss * a.in_balance[c] : 0.0f;
+  }
+  const int64_t stride = (int64_t)gridDim.x * kWaves * kRows;
+  for (int64_t base = ((int64_t)blockIdx.x * kWaves + wave) * kRows; base < a.rows; base += stride) {
+    const int64_t row = base + lane / G;
+    const bool in = row < a.rows;
+    const bool part = in && a.in_chosen[row * a.topk] >= 0;
+    const T* zr = static_cast<const T*>(a.z) + (part ? row : 0) * a.ld;
+    const float lse = part ? a.in_lse[row] : 0.0f;
+    float z[V];
+    load_logits<T, G, V, U>(zr, part ? a.experts : 0, gl, -INFINITY, z);
+    float p[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      p[v] = exp_fast(z[v] - lse);
+
+    // lane j of the group works out d_j, d_{j + G}, ... of the chosen experts
+    int32_t idx[kKeep];
+    float d[kKeep], pc[kKeep], dg = 0.0f, total = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kKeep; ++i) {
+      const int j = i * G + gl;
+      idx[i] = -1;
+      d[i] = pc[i] = 0.0f;
+      if (part && j < a.topk) {
+        const int32_t e = a.in_chosen[row * a.topk + j];
+        if (e >= 0 && e < a.experts) {
+          idx[i] = e;
+          float f[1];
+          unpack(zr + e, f);
+          pc[i] = exp_fast(f[0] - lse);
+          if (a.dgates != nullptr) {
+            d[i] = a.dgates[row * a.topk + j];
+            dg += d[i] * a.in_gates[row * a.topk + j];
+          }
+          total += pc[i];
+        }
+      }
+    }
+    if (a.normalize) {
+      dg = lanes_sum<G>(dg);
+      total = lanes_sum<G>(total);
+#pragma unroll
+      for (int i = 0; i < kKeep; ++i)
+        d[i] = idx[i] >= 0 && a.dgates != nullptr ? (d[i] - dg) / total : 0.0f;
+    }
+    float along = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kKeep; ++i)
+      along += pc[i] * d[i];
+    float dp[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      dp[v] = bal[v];
+      along += p[v] * bal[v];
+    }
+    along = lanes_sum<G>(along);
+    if (a.dgates != nullptr) {
+      for (int j = 0; j < a.topk; ++j) {
+        int32_t e = -1;
+        float dj = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kKeep; ++i)
+          if (i == j / G) {
+            e = __shfl(idx[i], j % G, G);
+            dj = __shfl(d[i], j % G, G);
+          }
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+          dp[v] += router_col<G, U>(v, gl) == e ? dj : 0.0f;
+      }
+    }
+    if (in) {
+      T* dr = static_cast<T*>(a.dz) + row * a.experts;
+#pragma unroll
+      for (int q = 0; q < V / U; ++q) {
+        const int c = router_col<G, U>(q * U, gl);
+        float f[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+          const int v = q * U + i;
+          // a closed expert's p is 0 and stays so
+          f[i] = part ? p[v] * (dp[v] - along) : 0.0f;
+        }
+        if (c < a.experts)
+          store(dr + c, f);
+      }
+    }
+  }
+}
+
+static int64_t router_rows_per_block(int64_t experts, int waves) { return (experts <= 256 ? 4 : 1) * (int64_t)waves; }
+static int64_t router_blocks(int64_t rows, int64_t experts) {
+  const int64_t per = router_rows_per_block(experts, kRouterWaves);
+  const int64_t want = (rows + per - 1) / per;
+  return want < 1 ? 1 : want < kRouterBlocks ? want : kRouterBlocks;
+}
+
+int64_t router_workspace_bytes(int64_t rows, int64_t experts) {
+  const int64_t blocks = router_blocks(rows, experts);
+  return blocks == 1 ? 0 : blocks * (8 * experts + 4);
+}
+
+template <typename T, int G, int V, int U>
+static hipError_t launch_router(const RouterArgs& a, bool bwd, int64_t blocks, hipStream_t stream) {
+  if (bwd) {
+    hipLaunchKernelGGL((router_bwd_kernel<T, G, V, U>), dim3((unsigned)blocks), dim3(kRouterBwdThreads), 0, stream, a);
+    return hipGetLastError();
+  }
+  hipLaunchKernelGGL((router_fwd_kernel<T, G, V, U>), dim3((unsigned)blocks), dim3(kRouterThreads), 0, stream, a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || blocks == 1)
+    return e;
+  hipLaunchKernelGGL(router_fold_kernel, dim3(1), dim3(kRouterThreads), 0, stream, a, (int32_t)blocks);
+  return hipGetLastError();
+}
+
+// Logits to a lane: the smallest power of two that holds the row, at least a
+// 16-byte word's worth on the wide path.
+template <typename T, int U>
+static hipError_t launch_router_width(const RouterArgs& a, bool bwd, int64_t blocks, hipStream_t stream) {
+  if (a.experts <= 256) {
+    if constexpr (U == 1) {
+      if (a.experts <= 16)
+        return launch_router<T, 16, 1, U>(a, bwd, blocks, stream);
+      if (a.experts <= 32)
+        return launch_router<T, 16, 2, U>(a, bwd, blocks, stream);
+    }
+    if constexpr (U <= 4) {
+      if (a.experts <= 64)
+        return launch_router<T, 16, 4, U>(a, bwd, blocks, stream);
+    }
+    if (a.experts <= 128)
+      return launch_router<T, 16, 8, U>(a, bwd, blocks, stream);
+    return launch_router<T, 16, 16, U>(a, bwd, blocks, stream);
+  }
+  if (a.experts <= 512)
+    return launch_router<T, 64, 8, U>(a, bwd, blocks, stream);
+  return launch_router<T, 64, 16, U>(a, bwd, blocks, stream);
+}
+
+static hipError_t launch_router_any(const RouterArgs& a, bool f32, bool vec, bool bwd, int64_t blocks,
+                                    hipStream_t stream) {
+  // rows of at most 32 experts fit single loads
+  vec = vec && a.experts > 32;
+  if (f32)
+    return vec ? launch_router_width<float, 4>(a, bwd, blocks, stream)
+               : launch_router_width<float, 1>(a, bwd, blocks, stream);
+  return vec ? launch_router_width<uint16_t, 8>(a, bwd, blocks, stream)
+             : launch_router_width<uint16_t, 1>(a, bwd, blocks, stream);
+}
+
+hipError_t launch_router_fwd(const void* logits, int64_t ld, bool f32, const uint8_t* valid, int64_t rows,
+                             int32_t experts, int32_t topk, bool normalize, int32_t align, int32_t* chosen,
+                             float* gates, float* lse, int32_t* counts, int32_t* ends, float* balance, float* loss,
+                             void* workspace, bool vec, hipStream_t stream) {
+  RouterArgs a = {};
+  a.z = logits, a.ld = ld, a.rows = rows, a.valid = valid, a.experts = experts, a.topk = topk;
+  a.normalize = normalize, a.align = align, a.chosen = chosen, a.gates = gates, a.lse = lse, a.counts = counts;
+  a.ends = ends, a.balance = balance, a.loss = loss;
+  const int64_t blocks = router_blocks(rows, experts);
+  a.part_p = static_cast<float*>(workspace);
+  a.part_n = reinterpret_cast<int32_t*>(a.part_p + blocks * experts);
+  a.part_rows = a.part_n + blocks * experts;
+  return launch_router_any(a, f32, vec, false, blocks, stream);
+}
+
+hipError_t launch_router_bwd(const void* logits, int64_t ld, bool f32, const float* lse, const int32_t* chosen,
+                             const float* gates, const float* balance, const float* dgates, const float* dloss,
+                             int64_t rows, int32_t experts, int32_t topk, bool normalize, void* dlogits, bool vec,
+                             hipStream_t stream) {
+  RouterArgs a = {};
+  a.z = logits, a.ld = ld, a.rows = rows, a.experts = experts, a.topk = topk, a.normalize = normalize;
+  a.in_lse = lse, a.in_chosen = chosen, a.in_gates = gates, a.in_balance = balance, a.dgates = dgates;
+  a.dloss = dloss, a.dz = dlogits;
+  const int64_t per = router_rows_per_block(experts, kRouterBwdThreads / 64);
+  const int64_t want = (rows + per - 1) / per;
+  return launch_router_any(a, f32, vec, true, want < 2048 ? want : 2048, stream);
+}
+
+}  // namespace mx

@@ -1,0 +1,159 @@
+// Device helpers shared by the training-step operators (gfx950 only): moves
+// between bf16 / binary32 memory and binary32 registers, and sums and maxima
+// over lanes.  All arithmetic is binary32.
+#pragma once
+
+#include "mx_device.h"
+
+namespace mx {
+
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+// Two binary32 values -> packed bf16, nearest-even, the first in the low half
+// (one v_cvt_pk_bf16_f32).
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2){lo, hi}, bf16x2));
+}
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+// T: float, or uint16_t for bf16 bits.  N consecutive elements <-> binary32.
+// N > 1 moves whole 16-byte words (N * sizeof(T) a multiple of 16, aligned),
+// except for eight-byte halves of bf16 (N = 4).
+template <int N>
+__device__ __forceinline__ void unpack(const float* p, float (&f)[N]) {
+  if constexpr (N == 1) {
+    f[0] = *p;
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+      const f32x4 v = *reinterpret_cast<const f32x4*>(p + i);
+      f[i] = v[0], f[i + 1] = v[1], f[i + 2] = v[2], f[i + 3] = v[3];
+    }
+  }
+}
+template <int N>
+__device__ __forceinline__ void unpack(const uint16_t* p, float (&f)[N]) {
+  if constexpr (N == 1) {
+    f[0] = bf16_lo(*p);
+  } else if constexpr (N == 4) {
+    const u32x2 v = *reinterpret_cast<const u32x2*>(p);
+    f[0] = bf16_lo(v[0]), f[1] = bf16_hi(v[0]), f[2] = bf16_lo(v[1]), f[3] = bf16_hi(v[1]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; i += 8) {
+      const u32x4 v = *reinterpret_cast<const u32x4*>(p + i);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        f[i + 2 * j] = bf16_lo(v[j]), f[i + 2 * j + 1] = bf16_hi(v[j]);
+    }
+  }
+}
+
+// N elements as loaded, one register word per 4 bytes (a bf16 single fills
+// one word): kept raw while in flight, turned into binary32 when used.
+template <typename T, int N>
+struct Raw {
+  static constexpr int kWords = N == 1 ? 1 : N * (int)sizeof(T) / 4;
+  uint32_t w[kWords];
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i)
+      w[i] = 0;
+  }
+  __device__ __forceinline__ void load(const T* p) {
+    if constexpr (N == 1) {
+      if constexpr (sizeof(T) == 2)
+        w[0] = *p;
+      else
+        w[0] = __float_as_uint(*p);
+    } else {
+      static_assert(N * sizeof(T) == 16, "one 16-byte word");
+      const u32x4 v = *reinterpret_cast<const u32x4*>(p);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        w[i] = v[i];
+    }
+  }
+  __device__ __forceinline__ float get(int i) const {
+    if constexpr (sizeof(T) == 4)
+      return __uint_as_float(w[i]);
+    else if constexpr (N == 1)
+      return bf16_lo(w[0]);
+    else
+      return (i & 1) ? bf16_hi(w[i / 2]) : bf16_lo(w[i / 2]);
+  }
+};
+
+// N binary32 values -> memory as T, rounded to nearest-even where T is bf16.
+template <typename T, int N>
+__device__ __forceinline__ void store(T* p, const float (&f)[N]) {
+  if constexpr (sizeof(T) == 4) {
+    if constexpr (N == 1) {
+      *p = f[0];
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; i += 4)
+        *reinterpret_cast<f32x4*>(p + i) = (f32x4){f[i], f[i + 1], f[i + 2], f[i + 3]};
+    }
+  } else {
+    if constexpr (N == 1) {
+      *p = (uint16_t)bf16_pair(f[0], f[0]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; i += 8)
+        *reinterpret_cast<u32x4*>(p + i) = (u32x4){bf16_pair(f[i], f[i + 1]), bf16_pair(f[i + 2], f[i + 3]),
+                                                   bf16_pair(f[i + 4], f[i + 5]), bf16_pair(f[i + 6], f[i + 7])};
+    }
+  }
+}
+
+// Lane moves inside rows of 16 lanes whose four steps visit every lane:
+// neighbour, neighbouring pair, other half of 8, other half of 16.
+template <int STEP>
+__device__ __forceinline__ uint32_t row16_move(uint32_t v) {
+  constexpr int ctrl = STEP == 0 ? 0xB1 : STEP == 1 ? 0x4E : STEP == 2 ? 0x141 : 0x140;
+  return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, ctrl, 0xF, 0xF, false);
+}
+
+// op over the G lanes (16 or 64, aligned) a lane belongs to; every lane gets
+// the result, the same bits in each (op is commutative and every step pairs
+// lanes symmetrically).
+template <int G, class Op>
+__device__ __forceinline__ uint32_t lanes_reduce(uint32_t v, Op op) {
+  v = op(v, row16_move<0>(v));
+  v = op(v, row16_move<1>(v));
+  v = op(v, row16_move<2>(v));
+  v = op(v, row16_move<3>(v));
+  if constexpr (G == 64) {
+    const auto a = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    v = op(a[0], a[1]);
+    const auto b = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    v = op(b[0], b[1]);
+  } else {
+    static_assert(G == 16, "lanes of a group");
+  }
+  return v;
+}
+template <int G = 64>
+__device__ __forceinline__ float lanes_sum(float v) {
+  return __uint_as_float(lanes_reduce<G>(__float_as_uint(v), [](uint32_t a, uint32_t b) {
+    return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
+  }));
+}
+template <int G>
+__device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
+  return lanes_reduce<G>(v, [](uint32_t a, uint32_t b) { return max(a, b); });
+}
+template <int G>
+__device__ __forceinline__ uint32_t lanes_min(uint32_t v) {
+  return lanes_reduce<G>(v, [](uint32_t a, uint32_t b) { return min(a, b); });
+}
+
+// e^x from the hardware's 2^x: the product with log2(e) is rounded once, so
+// the relative error grows like |x| * 2^-24, on top of the one or two ulp of
+// v_exp_f32.
+__device__ __forceinline__ float exp_fast(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504088896341f); }
+
+}  // namespace mx
