@@ -34,6 +34,8 @@
 #include "mx_train_launch.h"
 #include "mxtrain.h"
 
+#include <type_traits>
+
 namespace mx {
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
@@ -68,6 +70,23 @@ __device__ __forceinline__ void group_range(const int32_t* ends, int g, int32_t 
   run = (int32_t)lanes_max<64>((uint32_t)run);   // not negative
   lo = __builtin_amdgcn_readfirstlane(min(run, rows));
   hi = __builtin_amdgcn_readfirstlane(min(max(run, ends[g]), rows));
+}
+
+// 16 bytes per lane from memory into LDS, in lane order from `to` on (the same
+// in every lane).  As the compiler's own form of it, every later read from LDS
+// would wait for the load, since the transposing reads carry nothing that
+// tells the two halves apart; here the caller waits (vmcnt) and meets the
+// other waves at a barrier before anything is read.  (m0, which holds the LDS
+// address, is not a register the compiler keeps values in.)
+__device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t rsrc, const uint8_t* to, int offset) {
+  const uint32_t at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const uint8_t*)to;
+  asm volatile(
+      "s_mov_b32 m0, %0\n\t"
+      "s_nop 0\n\t"
+      "buffer_load_dwordx4 %1, %2, 0 offen lds"
+      :
+      : "s"(__builtin_amdgcn_readfirstlane(at)), "v"(offset), "s"(rsrc)
+      : "memory");
 }
 
 template <bool VEC, bool BF16>
@@ -112,10 +131,14 @@ __global__ __launch_bounds__(kWgThreads) void wgrad_kernel(WgradArgs a) {
   const int drow = 2 * wave + lane / 32;
   const int dchunk = (lane % 32) ^ ((drow & 3) << 2);
   const int xrow = t / 16, xcol = 16 * (t % 16);
+  const int x_at = xrow * kWgRow + 16 * (((xcol / 8) ^ ((xrow & 3) << 2)) ^ ((xcol / 8) >> 4));   // the other chunk: ^ 16
+  const int64_t dy_last = (int64_t)(a.rows - 1) * a.lddy + a.n;   // elements of dy
   u32x4 codes[4], dreg[VEC ? 1 : 8];
   uint32_t scales[4];
 
-  auto load_stage = [&](int st, int buf) {
+  // dy of stage st: straight into LDS half h, or into registers.
+  auto load_dy = [&](auto h_c, int st) {
+    constexpr int h = decltype(h_c)::value;
     const int32_t m0 = lo + st * kWgTokens;
     const int32_t left = min(hi - m0, kWgTokens);   // may be <= 0: nothing in range
     if constexpr (VEC) {
@@ -123,26 +146,30 @@ __global__ __launch_bounds__(kWgThreads) void wgrad_kernel(WgradArgs a) {
       const __amdgpu_buffer_rsrc_t rd = buffer_rsrc(a.dy + (left > 0 ? m0 : 0) * a.lddy + i0, (uint32_t)bytes);
 #pragma unroll
       for (int u = 0; u < 8; ++u)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(
-            rd, (__attribute__((address_space(3))) void*)(lds[buf][0] + (8 * u + 2 * wave) * kWgRow), 16,
-            (8 * u + drow) * (int)a.lddy * 2 + 16 * dchunk, 0, 0, 0);
+        load_to_lds(rd, lds[h][0] + (8 * u + 2 * wave) * kWgRow, (8 * u + drow) * (int)a.lddy * 2 + 16 * dchunk);
     } else {
+      // 16 bytes at any alignment; what lies past column n belongs to columns
+      // that are not stored.  Only at the very end of dy, element by element.
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
         const int row = 8 * u + drow;
         const int64_t c = i0 + 8 * dchunk;
         dreg[u] = (u32x4){0, 0, 0, 0};
         if (row < left && c < a.n) {
-          const uint16_t* p = a.dy + (int64_t)(m0 + row) * a.lddy + c;
-          if (c + 8 <= a.n) {
-            dreg[u] = *reinterpret_cast<const u32x4_any*>(p);
+          const int64_t at = (int64_t)(m0 + row) * a.lddy + c;
+          if (at + 8 <= dy_last) {
+            dreg[u] = *reinterpret_cast<const u32x4_any*>(a.dy + at);
           } else {
-            for (int e = 0; e < a.n - c; ++e)
-              dreg[u][e / 2] |= (uint32_t)p[e] << (16 * (e & 1));
+            for (int e = 0; e < dy_last - at; ++e)
+              dreg[u][e / 2] |= (uint32_t)a.dy[at + e] << (16 * (e & 1));
           }
         }
       }
     }
+  };
+  auto load_codes = [&](int st) {
+    const int32_t m0 = lo + st * kWgTokens;
+    const int32_t left = min(hi - m0, kWgTokens);
     const int64_t qbytes = left > 0 ? (left - 1) * a.k + (a.k - j0) : 0;
     const int64_t sbytes = left > 0 ? (left - 1) * ks + (ks - j0 / MX_BLOCK) : 0;
     const __amdgpu_buffer_rsrc_t rq = buffer_rsrc(a.q + (left > 0 ? m0 : 0) * a.k + j0, (uint32_t)qbytes);
@@ -153,27 +180,25 @@ __global__ __launch_bounds__(kWgThreads) void wgrad_kernel(WgradArgs a) {
       scales[u] = __builtin_amdgcn_raw_buffer_load_b8(rs, (16 * u + xrow) * (int)ks + xcol / MX_BLOCK, 0, 0);
     }
   };
-  // Codes (and dy where it came through registers) into LDS as bf16.
-  auto put_stage = [&](int buf) {
+  // Half e (eight codes) of code load u into LDS half h as bf16.
+  auto put_codes = [&](auto h_c, int u, int e) {
+    constexpr int h = decltype(h_c)::value;
+    const float sc = __uint_as_float(scales[u] << 23);
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      w[2 * i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes[u][2 * e + i], sc, false));
+      w[2 * i + 1] =
+          __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes[u][2 * e + i], sc, true));
+    }
+    *reinterpret_cast<u32x4*>(lds[h][1] + 16 * u * kWgRow + (x_at ^ (16 * e))) = (u32x4){w[0], w[1], w[2], w[3]};
+  };
+  auto put_dy = [&](auto h_c) {
+    constexpr int h = decltype(h_c)::value;
     if constexpr (!VEC) {
 #pragma unroll
       for (int u = 0; u < 8; ++u)
-        *reinterpret_cast<u32x4*>(lds[buf][0] + (8 * u + drow) * kWgRow + 16 * (lane % 32)) = dreg[u];
-    }
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const float sc = __uint_as_float(scales[u] << 23);
-      uint32_t w[8];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        w[2 * i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes[u][i], sc, false));
-        w[2 * i + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes[u][i], sc, true));
-      }
-      const int row = 16 * u + xrow;
-      uint8_t* base = lds[buf][1] + row * kWgRow;
-      const int c = xcol / 8, x = (row & 3) << 2;
-      *reinterpret_cast<u32x4*>(base + 16 * (c ^ x)) = (u32x4){w[0], w[1], w[2], w[3]};
-      *reinterpret_cast<u32x4*>(base + 16 * ((c + 1) ^ x)) = (u32x4){w[4], w[5], w[6], w[7]};
+        *reinterpret_cast<u32x4*>(lds[h][0] + (8 * u + drow) * kWgRow + 16 * (lane % 32)) = dreg[u];
     }
   };
 
@@ -185,39 +210,90 @@ __global__ __launch_bounds__(kWgThreads) void wgrad_kernel(WgradArgs a) {
 #pragma unroll
   for (int b = 0; b < kWgBlocks; ++b) {
     a_at[b] = tok * kWgRow + 64 * ((4 * wi + b) ^ (tok & 3)) + sub;
-    b_at[b] = tok * kWgRow + 64 * ((4 * wj + b) ^ (tok & 3)) + sub;
+    b_at[b] = tok * kWgRow + 64 * ((4 * wj + b) ^ (tok & 3)) + (sub ^ (16 * wj));
   }
   typedef __attribute__((address_space(3))) s16x4* lds_s16x4;
-  auto operand = [&](const uint8_t* base, int at) {
-    const s16x4 lo4 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(base + at));
-    const s16x4 hi4 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(base + at + 4 * kWgRow));
-    return __builtin_bit_cast(bf16x8, (s16x8)__builtin_shufflevector(lo4, hi4, 0, 1, 2, 3, 4, 5, 6, 7));
+  typedef s16x4 Step[2 * kWgBlocks][2];   // operands of 16 tokens: dy blocks, then x blocks, two reads each
+  // Read r (0 .. 15) of step `step` from LDS half h, in the order the MFMAs
+  // use the operands: dy 0, x 0 .. 3, dy 1 .. 3.
+  auto read_one = [&](auto h_c, int step, int r, Step& f) {
+    constexpr int h = decltype(h_c)::value;
+    const int o = r / 2, e = r % 2;
+    const bool is_x = o >= 1 && o <= kWgBlocks;
+    const int b = o == 0 ? 0 : is_x ? o - 1 : o - kWgBlocks;
+    const int at = (is_x ? b_at[b] : a_at[b]) + (16 * step + 4 * e) * kWgRow;
+    f[is_x ? kWgBlocks + b : b][e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(lds[h][is_x] + at));
+  };
+  auto operand = [](const s16x4 (&f)[2]) {
+    return __builtin_bit_cast(bf16x8, (s16x8)__builtin_shufflevector(f[0], f[1], 0, 1, 2, 3, 4, 5, 6, 7));
+  };
+  auto mfma = [&](int m, const Step& f) {
+    const int i = m / kWgBlocks, j = m % kWgBlocks;
+    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(operand(f[i]), operand(f[kWgBlocks + j]), acc[i][j], 0, 0, 0);
   };
 
-  if (stages > 0)
-    load_stage(0, 0);
-  for (int st = 0; st < stages; ++st) {
-    const int buf = st & 1;
-    __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0): this wave's loads of the stage
-    put_stage(buf);
-    // after this barrier the stage is whole, and nobody reads the other half
-    lds_barrier();
-    if (st + 1 < stages)
-      load_stage(st + 1, buf ^ 1);
+  // A stage is four steps of 16 tokens, 16 MFMAs each; there is one wave to a
+  // SIMD, so nothing but this order hides a wait.  While a step's MFMAs run,
+  // the next step's operands are read from LDS, two reads after each of the
+  // first eight.  Before step 2 the wave waits for its loads of the next
+  // stage, which have had three steps; step 2 turns the codes into bf16 in the
+  // other LDS half.  The reads and writes of step 2 are done a few MFMAs
+  // before its end, so that the stage's one barrier, between steps 2 and 3,
+  // costs little.  Step 3 reads the next stage's first operands, and the loads
+  // of the stage after that go into the half that the barrier has freed.
+  auto stage = [&](auto h_c, int st, Step& f0, Step& f1) {
+    constexpr int h = decltype(h_c)::value;
+    using H = std::integral_constant<int, h>;
+    using O = std::integral_constant<int, h ^ 1>;
+    constexpr int kM = kWgBlocks * kWgBlocks;
+    auto step = [&](auto from, int next, const Step& now, Step& then, bool put) {
 #pragma unroll
-    for (int step = 0; step < kWgTokens / 16; ++step) {
-      bf16x8 fa[kWgBlocks], fb[kWgBlocks];
-#pragma unroll
-      for (int b = 0; b < kWgBlocks; ++b) {
-        fa[b] = operand(lds[buf][0] + 16 * step * kWgRow, a_at[b]);
-        fb[b] = operand(lds[buf][1] + 16 * step * kWgRow, b_at[b]);
+      for (int m = 0; m < kM; ++m) {
+        mfma(m, now);
+        if (m < kM / 2) {
+          read_one(from, next, 2 * m, then);
+          read_one(from, next, 2 * m + 1, then);
+        }
+        if (put && m >= 4 && m < 12)
+          put_codes(O(), (m - 4) / 2, (m - 4) % 2);
+        __builtin_amdgcn_sched_barrier(0);
       }
+    };
+    step(H(), 1, f0, f1, false);
+    step(H(), 2, f1, f0, false);
+    __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0)
+    put_dy(O());
+    step(H(), 3, f0, f1, true);
+    lds_barrier();
+    load_dy(H(), st + 2);
+    load_codes(st + 2);
+    __builtin_amdgcn_sched_barrier(0);
+    step(O(), 0, f1, f0, false);
+  };
+  if (stages > 0) {
+    using S0 = std::integral_constant<int, 0>;
+    using S1 = std::integral_constant<int, 1>;
+    Step f0, f1;
+    load_dy(S0(), 0);
+    load_codes(0);
+    __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0)
 #pragma unroll
-      for (int i = 0; i < kWgBlocks; ++i)
+    for (int u = 0; u < 8; ++u)
+      put_codes(S0(), u / 2, u % 2);
+    put_dy(S0());
+    load_dy(S1(), 1);
+    load_codes(1);
+    lds_barrier();
 #pragma unroll
-        for (int j = 0; j < kWgBlocks; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[i], fb[j], acc[i][j], 0, 0, 0);
+    for (int r = 0; r < 4 * kWgBlocks; ++r)
+      read_one(S0(), 0, r, f0);
+    // stages past the last (an odd count runs one) load zeros and add nothing
+    for (int st = 0; st < stages; st += 2) {
+      stage(S0(), st, f0, f1);
+      stage(S1(), st + 1, f0, f1);
     }
+    // loads into LDS still in flight must land before it is used again
+    __builtin_amdgcn_s_waitcnt(0x0F70);
   }
 
   // register v of lane l: row 8 (v / 4) + 4 (l / 32) + v % 4, column l % 32
