@@ -64,27 +64,115 @@ constexpr int kWgS = kWgX + kWgTokens * kWgTile;     // where the scales start: 
 constexpr int kWgScaleRow = 4 * kWgTokens + 16;      // (16 more than the banks' period)
 constexpr int kWgSlot = kWgS + kWgTile / MX_BLOCK * kWgScaleRow + 128;
 constexpr int kWgSlots = 3;
+constexpr int kWgCus = 256;
 static_assert(kWgSlot % 256 == 0 && kWgSlots * kWgSlot <= 160 * 1024, "stages fit LDS");
 
 struct WgradArgs {
   const uint16_t* dy;
   const uint8_t *q, *s;
   const int32_t* ends;
-  void* out;          // dw, or the pieces' sums
+  void* out;
+  float* part;        // sums of pieces, a 256 x 256 tile each
   int64_t lddy, n, k;
-  int32_t rows, groups, splits;
-  uint32_t tiles_n, tiles_k, per_xcd, total;
+  int32_t rows, groups;
+  uint32_t tiles_n, tiles_k;
+  // One group: the first `whole` tiles are not cut, the others into `pieces`.
+  // Several: `pieces` slots for groups or pieces of groups, a piece being
+  // `piece_stages` long or thereabouts.
+  uint32_t whole, pieces;
+  int32_t piece_stages;
 };
 
-// Token range of group g: [min(max(0, ends_0 .. ends_{g-1}), rows), min(max(0,
-// ends_0 .. ends_g), rows)), found by one wave's lanes together.
-__device__ __forceinline__ void group_range(const int32_t* ends, int g, int32_t rows, int32_t& lo, int32_t& hi) {
-  int32_t run = 0;
-  for (int i = threadIdx.x & 63; i < g; i += 64)
-    run = max(run, ends[i]);
-  run = (int32_t)lanes_max<64>((uint32_t)run);   // not negative
-  lo = __builtin_amdgcn_readfirstlane(min(run, rows));
-  hi = __builtin_amdgcn_readfirstlane(min(max(run, ends[g]), rows));
+// What a workgroup works on: a tile of group g over tokens [lo, hi), into the
+// output (part < 0) or into tile `part` of the pieces' sums.
+struct WgradItem {
+  int32_t g, lo, hi, part;
+};
+
+// Pieces of a group of `stages` stages, and the token range of one.
+__device__ __forceinline__ int32_t group_pieces(int32_t stages, int32_t piece_stages) {
+  return max(1, (stages + piece_stages / 2) / piece_stages);
+}
+__device__ __forceinline__ void piece_range(int32_t pieces, int32_t piece, int32_t& lo, int32_t& hi) {
+  const int32_t stages = (hi - lo + kWgTokens - 1) / kWgTokens, each = (stages + pieces - 1) / pieces;
+  const int32_t first = min(piece * each, stages);
+  hi = min((int64_t)hi, (int64_t)lo + (int64_t)min(first + each, stages) * kWgTokens);
+  lo = min((int64_t)hi, (int64_t)lo + (int64_t)first * kWgTokens);
+}
+
+// The groups' schedule, found by one wave with a group to a lane: which group
+// and piece has slot `slot` (by_slot), or is the slot-th of the groups that
+// are cut.  Group g's tokens are [min(max(0, ends_0 .. ends_{g-1}), rows),
+// min(max(0, ends_0 .. ends_g), rows)).  Up to 64 groups come longest piece
+// first, more in their own order.  Returns false past the last; g, lo, hi are
+// the group's, `first_part` the number of pieces of cut groups before it.
+__device__ __forceinline__ bool find_slot(const WgradArgs& a, int32_t slot, bool by_slot, int32_t& g, int32_t& lo,
+                                          int32_t& hi, int32_t& pieces, int32_t& piece, int32_t& first_part) {
+  const int lane = threadIdx.x & 63;
+  int32_t run = 0, slots = 0, parts = 0, cuts = 0;   // of the groups before these 64
+  for (int32_t g0 = 0; g0 < a.groups; g0 += 64) {
+    const bool on = g0 + lane < a.groups;
+    int32_t end = on ? max(a.ends[g0 + lane], 0) : 0;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int32_t o = __shfl_up(end, d);
+      if (lane >= d)
+        end = max(end, o);
+    }
+    end = min(max(end, run), a.rows);
+    const int32_t up = __shfl_up(end, 1);
+    const int32_t begin = lane == 0 ? min(run, a.rows) : up;
+    run = __builtin_amdgcn_readlane(end, 63);
+    const int32_t stages = (end - begin + kWgTokens - 1) / kWgTokens;
+    const int32_t count = on ? group_pieces(stages, a.piece_stages) : 0;
+    const int32_t len = (stages + max(count, 1) - 1) / max(count, 1);
+    int32_t my_slots = 0, my_parts = 0, my_cuts = 0;
+    const int n = min(a.groups - g0, 64);
+    for (int q = 0; q < n; ++q) {
+      const int32_t c = __builtin_amdgcn_readlane(count, q), l = __builtin_amdgcn_readlane(len, q);
+      const bool before = a.groups <= 64 ? l > len || (l == len && q < lane) : q < lane;
+      if (before) {
+        my_slots += c;
+        my_parts += c > 1 ? c : 0;
+        my_cuts += c > 1;
+      }
+    }
+    my_slots += slots, my_parts += parts, my_cuts += cuts;
+    const bool hit = by_slot ? on && my_slots <= slot && slot < my_slots + count : on && count > 1 && my_cuts == slot;
+    const uint64_t at = __ballot(hit);
+    if (at != 0) {
+      const int src = __builtin_ctzll(at);
+      g = g0 + src;
+      lo = __builtin_amdgcn_readlane(begin, src);
+      hi = __builtin_amdgcn_readlane(end, src);
+      pieces = __builtin_amdgcn_readlane(count, src);
+      piece = slot - __builtin_amdgcn_readlane(my_slots, src);
+      first_part = __builtin_amdgcn_readlane(my_parts, src);
+      return true;
+    }
+    for (int q = 0; q < n; ++q) {
+      const int32_t c = __builtin_amdgcn_readlane(count, q);
+      slots += c;
+      parts += c > 1 ? c : 0;
+      cuts += c > 1;
+    }
+  }
+  return false;
+}
+
+// Blocks of a segment of `tiles` tiles, and the tile of its block b, or -1.
+// The workgroups of an XCD (every eighth) take neighbouring tiles, which share
+// operands in its L2; few tiles go to the XCDs in turn instead, so that none
+// is left without.
+constexpr uint32_t kWgSpread = 64;
+__host__ __device__ inline uint32_t segment_blocks(uint32_t tiles) {
+  return tiles % 8 == 0 || tiles < kWgSpread ? tiles : (tiles + 7) / 8 * 8;
+}
+__device__ __forceinline__ int32_t segment_tile(uint32_t tiles, uint32_t b) {
+  if (tiles % 8 != 0 && tiles < kWgSpread)
+    return (int32_t)b;
+  const uint32_t tile = b % 8 * ((tiles + 7) / 8) + b / 8;
+  return tile < tiles ? (int32_t)tile : -1;
 }
 
 // 16 bytes per lane, or one byte widened to a dword, from memory into LDS, in
@@ -137,23 +225,39 @@ __device__ __forceinline__ void wait_loads() {
 template <bool VEC, bool BF16>
 __global__ __launch_bounds__(kWgThreads) __attribute__((amdgpu_waves_per_eu(1, 1))) void wgrad_kernel(WgradArgs a) {
   __shared__ __attribute__((aligned(256))) uint8_t lds[kWgSlots * kWgSlot];
-  const uint32_t id = (blockIdx.x % 8) * a.per_xcd + blockIdx.x / 8;
-  if (id >= a.total)
-    return;   // uniform, before any barrier
   const uint32_t tiles = a.tiles_n * a.tiles_k;
-  const uint32_t piece = id / tiles, tile = id % tiles;
-  const int g = (int)(piece % (uint32_t)a.groups), split = (int)(piece / (uint32_t)a.groups);
-  const int64_t i0 = (int64_t)(tile / a.tiles_k) * kWgTile, j0 = (int64_t)(tile % a.tiles_k) * kWgTile;
-
-  int32_t lo = 0, hi = a.rows;
-  if (a.ends != nullptr)
-    group_range(a.ends, g, a.rows, lo, hi);
-  if (a.splits > 1) {
-    const int32_t each = ((hi - lo + a.splits - 1) / a.splits + kWgTokens - 1) / kWgTokens * kWgTokens;
-    const int64_t first = lo + (int64_t)split * each;
-    hi = (int32_t)min((int64_t)hi, first + each);
-    lo = (int32_t)min((int64_t)hi, first);
+  WgradItem it = {0, 0, a.rows, -1};
+  int32_t tile;
+  if (a.groups == 1) {
+    if (a.ends != nullptr)
+      it.hi = min(max(a.ends[0], 0), a.rows);
+    const uint32_t first = segment_blocks(a.whole);
+    if (blockIdx.x < first) {
+      tile = segment_tile(a.whole, blockIdx.x);
+    } else {
+      const uint32_t cut = tiles - a.whole, per = segment_blocks(cut), piece = (blockIdx.x - first) / per;
+      tile = segment_tile(cut, (blockIdx.x - first) % per);
+      it.part = tile < 0 ? 0 : (int32_t)(piece * cut + (uint32_t)tile);
+      tile = tile < 0 ? tile : tile + (int32_t)a.whole;
+      piece_range((int32_t)a.pieces, (int32_t)piece, it.lo, it.hi);
+    }
+  } else {
+    const uint32_t per = segment_blocks(tiles);
+    tile = segment_tile(tiles, blockIdx.x % per);
+    int32_t pieces, piece, first_part;
+    if (!find_slot(a, (int32_t)(blockIdx.x / per), true, it.g, it.lo, it.hi, pieces, piece, first_part))
+      return;   // uniform, before any barrier
+    if (pieces > 1) {
+      it.part = (first_part + piece) * (int32_t)tiles + max(tile, 0);
+      piece_range(pieces, piece, it.lo, it.hi);
+    }
   }
+  if (tile < 0)
+    return;
+  // values that came through vector registers, made scalar
+  const int32_t g = __builtin_amdgcn_readfirstlane(it.g), part = __builtin_amdgcn_readfirstlane(it.part);
+  const int32_t lo = __builtin_amdgcn_readfirstlane(it.lo), hi = __builtin_amdgcn_readfirstlane(it.hi);
+  const int64_t i0 = (int64_t)((uint32_t)tile / a.tiles_k) * kWgTile, j0 = (int64_t)((uint32_t)tile % a.tiles_k) * kWgTile;
 
   const int t = threadIdx.x;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
@@ -211,15 +315,14 @@ __global__ __launch_bounds__(kWgThreads) __attribute__((amdgpu_waves_per_eu(1, 1
     run_q.next();
     run_s.next();
   };
-  constexpr int kFirstLoad = VEC ? 0 : 8, kStageLoads = 14 - kFirstLoad;
-  auto load_stage = [&](int slot) {
+  constexpr int kFirstLoad = VEC ? 0 : 8, kStageLoads = 14 - kFirstLoad, kHalfLoads = kStageLoads / 2;
+  auto load_stage = [&](int slot, int loads) {
 #pragma unroll
-    for (int i = kFirstLoad; i < 14; ++i) {
+    for (int i = kFirstLoad; i < kFirstLoad + loads; ++i) {
       target(i, slot);
       asm volatile("s_nop 0");
       load(i);
     }
-    next_stage();
   };
   // dy at any alignment: through registers, 16 bytes at a time; what lies
   // past column n belongs to columns that are not stored.  Only at the very
@@ -322,19 +425,17 @@ __global__ __launch_bounds__(kWgThreads) __attribute__((amdgpu_waves_per_eu(1, 1
   // has been read by then, and its slot takes the loads of stage st + 3.
   // An MFMA takes 16 cycles, in which two or three other instructions issue:
   // the rest is spread out accordingly, the loads (which queue up when they
-  // come together, and hold up the MFMAs behind them) one to four MFMAs.
-  auto step = [&](int next, const Dy& now, Dy& then, auto first_c, int slot) __attribute__((always_inline)) {
+  // come together, and hold up the MFMAs behind them) one to eight MFMAs.
+  auto step = [&](int next, const Dy& now, Dy& then, auto first_c, int to) __attribute__((always_inline)) {
     constexpr bool first = decltype(first_c)::value;
     each(std::make_integer_sequence<int, kWgBlocks * kWgBlocks>(), [&](auto m_c) __attribute__((always_inline)) {
       constexpr int m = decltype(m_c)::value;
-      constexpr int i = m % 4 == 1 ? m / 4 + kFirstLoad : 14;
+      constexpr int i = m % 8 == 1 && m / 8 < kHalfLoads ? kFirstLoad + m / 8 + (first ? kHalfLoads : 0) : 14;
       if constexpr (i < 14)
-        if (!first)
-          target(i, slot);
+        target(i, to);
       mfma(m, now);
       if constexpr (i < 14)
-        if (!first)
-          load(i);
+        load(i);
       if constexpr (m < 12)
         convert_part(3, m);
       if constexpr (m >= 12 && m < 22)
@@ -349,7 +450,8 @@ __global__ __launch_bounds__(kWgThreads) __attribute__((amdgpu_waves_per_eu(1, 1
         convert_part((m - 28) / 12, (m - 28) % 12);
       if constexpr (m == 58) {
         if (first) {
-          put_dy(slot == 0 ? kWgSlots - 1 : slot - 1);   // stage st + 2, where dy comes through registers
+          next_stage();
+          put_dy(to);   // where dy comes through registers
           wait_loads<kStageLoads>();
           lds_barrier();
         }
@@ -364,10 +466,12 @@ __global__ __launch_bounds__(kWgThreads) __attribute__((amdgpu_waves_per_eu(1, 1
     load_dy(1);
     put_dy(1);
     load_dy(2);
-    load_stage(0);
-    load_stage(1);
-    load_stage(2);
-    wait_loads<2 * kStageLoads>();   // stage 0 has landed
+    load_stage(0, kStageLoads);
+    next_stage();
+    load_stage(1, kStageLoads);
+    next_stage();
+    load_stage(2, kHalfLoads);
+    wait_loads<kStageLoads + kHalfLoads>();   // stage 0 has landed
     lds_barrier();
 #pragma unroll
     for (int r = 0; r < 10; ++r)
@@ -380,7 +484,7 @@ __global__ __launch_bounds__(kWgThreads) __attribute__((amdgpu_waves_per_eu(1, 1
       convert_part(r / 12, r % 12);
     int slot = 0;
     for (int st = 0; st < stages; ++st) {
-      step(1, d0, d1, std::true_type(), slot);
+      step(1, d0, d1, std::true_type(), slot == 0 ? kWgSlots - 1 : slot - 1);
       load_dy(st + 3);
       const int to = slot + 1 == kWgSlots ? 0 : slot + 1;
       const int by = (to - slot) * kWgSlot;
@@ -390,7 +494,6 @@ __global__ __launch_bounds__(kWgThreads) __attribute__((amdgpu_waves_per_eu(1, 1
       for (int i = 0; i < kWgBlocks; ++i)
         d_at[i] += by;
       step(0, d1, d0, std::false_type(), slot);
-      next_stage();
       slot = to;
     }
     // loads into LDS still in flight must land before the workgroup ends
@@ -407,23 +510,26 @@ __global__ __launch_bounds__(kWgThreads) __attribute__((amdgpu_waves_per_eu(1, 1
   // Register v of lane l: row 4 (l / 16) + v of its block; the lane's 8 blocks
   // along k are 8 neighbouring columns.
   const int64_t col = j0 + 128 * wj + 8 * l16;
-  if (col >= a.k)
+  if (part < 0 && col >= a.k)
     return;
-  const int64_t plane = ((int64_t)split * a.groups + g) * a.n;
   constexpr int kBytes = BF16 ? 2 : 4;
   const bool whole = (reinterpret_cast<uintptr_t>(a.out) & 15) == 0;
 #pragma unroll
   for (int i = 0; i < kWgBlocks; ++i)
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
-      const int64_t row = i0 + 128 * wi + 16 * i + 4 * lg + v;
-      if (row >= a.n)
-        continue;
+      const int row = 128 * wi + 16 * i + 4 * lg + v;
       float f[8];
 #pragma unroll
       for (int j = 0; j < kWgBlocks; ++j)
         f[j] = acc[i][j][v];
-      void* at = static_cast<uint8_t*>(a.out) + ((plane + row) * a.k + col) * kBytes;
+      if (part >= 0) {
+        store(a.part + ((int64_t)part * kWgTile + row) * kWgTile + 128 * wj + 8 * l16, f);
+        continue;
+      }
+      if (i0 + row >= a.n)
+        continue;
+      void* at = static_cast<uint8_t*>(a.out) + (((int64_t)g * a.n + i0 + row) * a.k + col) * kBytes;
       if (whole) {
         if constexpr (BF16)
           store(static_cast<uint16_t*>(at), f);
@@ -441,83 +547,138 @@ __global__ __launch_bounds__(kWgThreads) __attribute__((amdgpu_waves_per_eu(1, 1
     }
 }
 
-// dw = the sum of the pieces, in order; four elements to a thread.
+// The cut tiles: dw = the sum of a tile's pieces, in their order.  A
+// workgroup adds up `rows` rows of a tile, four at a time, a thread four
+// columns.
 template <bool BF16>
-__global__ __launch_bounds__(256) void wgrad_fold_kernel(const float* part, int32_t splits, int64_t elems, void* dw) {
-  const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
-  if (at >= elems)
-    return;   // elems is a multiple of 32
-  f32x4 sum = *reinterpret_cast<const f32x4*>(part + at);
-#pragma unroll 4
-  for (int s = 1; s < splits; ++s)
-    sum += *reinterpret_cast<const f32x4*>(part + s * elems + at);
-  if constexpr (BF16) {
-    const u32x2 w = {bf16_pair(sum[0], sum[1]), bf16_pair(sum[2], sum[3])};
-    uint16_t* p = static_cast<uint16_t*>(dw) + at;
-    p[0] = (uint16_t)w[0], p[1] = (uint16_t)(w[0] >> 16), p[2] = (uint16_t)w[1], p[3] = (uint16_t)(w[1] >> 16);
+__global__ __launch_bounds__(256) void wgrad_fold_kernel(WgradArgs a, int32_t rows) {
+  const uint32_t tiles = a.tiles_n * a.tiles_k;
+  int32_t g = 0, pieces = (int32_t)a.pieces;
+  int64_t tile = blockIdx.y, part = blockIdx.y, stride = tiles - a.whole;   // first piece's part, parts from piece to piece
+  if (a.groups == 1) {
+    tile += a.whole;
   } else {
-    float* p = static_cast<float*>(dw) + at;
-    p[0] = sum[0], p[1] = sum[1], p[2] = sum[2], p[3] = sum[3];
+    int32_t lo, hi, piece, first_part;
+    if (!find_slot(a, (int32_t)blockIdx.z, false, g, lo, hi, pieces, piece, first_part))
+      return;
+    part += (int64_t)first_part * tiles;
+    stride = tiles;
+  }
+  const int64_t i0 = tile / a.tiles_k * kWgTile, j0 = tile % a.tiles_k * kWgTile;
+  const int col = (threadIdx.x & 63) * 4;
+  if (j0 + col >= a.k)
+    return;
+  const bool whole = (reinterpret_cast<uintptr_t>(a.out) & 15) == 0;
+  for (int row = blockIdx.x * rows + (threadIdx.x >> 6); row < (int)(blockIdx.x + 1) * rows && i0 + row < a.n; row += 4) {
+    const float* p = a.part + (part * kWgTile + row) * kWgTile + col;
+    f32x4 sum = *reinterpret_cast<const f32x4*>(p);
+#pragma unroll 8
+    for (int s = 1; s < pieces; ++s)
+      sum += *reinterpret_cast<const f32x4*>(p + s * stride * kWgTile * kWgTile);
+    const int64_t at = ((int64_t)g * a.n + i0 + row) * a.k + j0 + col;
+    if constexpr (BF16) {
+      const u32x2 w = {bf16_pair(sum[0], sum[1]), bf16_pair(sum[2], sum[3])};
+      uint16_t* o = static_cast<uint16_t*>(a.out) + at;
+      if (whole)
+        *reinterpret_cast<u32x2*>(o) = w;
+      else
+        o[0] = (uint16_t)w[0], o[1] = (uint16_t)(w[0] >> 16), o[2] = (uint16_t)w[1], o[3] = (uint16_t)(w[1] >> 16);
+    } else {
+      float* o = static_cast<float*>(a.out) + at;
+      if (whole)
+        *reinterpret_cast<f32x4*>(o) = sum;
+      else
+        o[0] = sum[0], o[1] = sum[1], o[2] = sum[2], o[3] = sum[3];
+    }
   }
 }
 
-static int64_t wgrad_tiles(int64_t n, int64_t k, int32_t groups) {
-  return ((n + kWgTile - 1) / kWgTile) * ((k + kWgTile - 1) / kWgTile) * groups;
-}
+// How a call is cut up, from its sizes alone.
+struct WgradPlan {
+  uint32_t tiles_n, tiles_k, whole, pieces;
+  int32_t piece_stages;
+  int64_t blocks, parts;   // workgroups; tiles of pieces' sums
+  uint32_t cut;            // one group: tiles that are cut; several: groups that may be
+};
 
-// Pieces of the token axis: enough to give every CU a tile, as long as a
-// piece keeps about four stages (of the groups' average length).
-static int32_t wgrad_splits(int64_t rows, int64_t n, int64_t k, int32_t groups) {
-  const int64_t tiles = wgrad_tiles(n, k, groups);
-  if (tiles == 0 || tiles > 128)
-    return 1;
-  const int64_t by_cus = 256 / tiles, by_rows = rows / groups / (4 * kWgTokens);
-  const int64_t s = by_cus < by_rows ? by_cus : by_rows;
-  return s < 1 ? 1 : (int32_t)s;
+// One workgroup fills a CU, so tiles run in rounds of 256.  One group: full
+// rounds keep their tiles whole; what is left over is cut along the tokens
+// into as many pieces as fill a round, but no more than balances the time
+// saved with the traffic of the pieces' sums (about 1.3 us a stage against
+// 0.13 us a piece and tile: pieces = sqrt(10 stages / tiles)).
+// Several groups: a group is cut where it is more than half as long again as
+// its share of the GPU (and of 24 stages); from eight rounds of tiles on, none.
+static WgradPlan wgrad_plan(int64_t rows, int64_t n, int64_t k, int32_t groups) {
+  WgradPlan p = {};
+  p.tiles_n = (uint32_t)((n + kWgTile - 1) / kWgTile), p.tiles_k = (uint32_t)((k + kWgTile - 1) / kWgTile);
+  const int64_t tiles = (int64_t)p.tiles_n * p.tiles_k;
+  const int64_t stages = (rows + kWgTokens - 1) / kWgTokens;
+  if (groups == 1) {
+    const int64_t cut = tiles % kWgCus;
+    int64_t pieces = 1;
+    if (cut > 0) {
+      while ((pieces + 1) * (pieces + 1) * cut <= 10 * stages && (pieces + 1) * cut <= kWgCus && 2 * (pieces + 1) <= stages)
+        ++pieces;
+    }
+    p.cut = pieces > 1 ? (uint32_t)cut : 0;
+    p.whole = (uint32_t)(tiles - p.cut), p.pieces = (uint32_t)pieces;
+    p.parts = p.cut * pieces;
+    p.blocks = segment_blocks(p.whole) + (int64_t)segment_blocks(p.cut) * pieces;
+    return p;
+  }
+  const int64_t total = rows / kWgTokens + groups;   // at most: every group may end in a partial stage
+  int64_t each = INT32_MAX / 2;
+  if (tiles * groups < 8 * kWgCus) {
+    each = (total * tiles + kWgCus - 1) / kWgCus;
+    each = each < 24 ? 24 : each;
+  }
+  p.piece_stages = (int32_t)each;
+  p.pieces = (uint32_t)(total / each + groups);
+  const int64_t parts = total * 4 / (3 * each);      // a cut group is at least 1.5 pieces long
+  p.cut = (uint32_t)(parts / 2);
+  p.parts = p.cut > 0 ? parts * tiles : 0;
+  p.blocks = (int64_t)segment_blocks((uint32_t)tiles) * p.pieces;
+  return p;
 }
 
 int64_t wgrad_workspace_bytes(int64_t rows, int64_t n, int64_t k, int32_t groups) {
-  const int32_t s = wgrad_splits(rows, n, k, groups);
-  return s > 1 ? s * groups * n * k * 4 : 0;
+  return wgrad_plan(rows, n, k, groups).parts * kWgTile * kWgTile * 4;
 }
 
 int64_t wgrad_grid_blocks(int64_t rows, int64_t n, int64_t k, int32_t groups) {
-  const int64_t total = wgrad_tiles(n, k, groups) * wgrad_splits(rows, n, k, groups);
-  return (total + 7) / 8 * 8;
+  return wgrad_plan(rows, n, k, groups).blocks;
 }
 
 hipError_t launch_wgrad(const void* dy, int64_t lddy, const uint8_t* q, const uint8_t* s, int64_t rows, int64_t n,
                         int64_t k, const int32_t* ends, int32_t groups, void* dw, bool bf16, float* workspace,
                         bool vec, hipStream_t stream) {
+  const WgradPlan p = wgrad_plan(rows, n, k, groups);
   WgradArgs a = {};
   a.dy = static_cast<const uint16_t*>(dy), a.lddy = lddy, a.q = q, a.s = s, a.ends = ends, a.n = n, a.k = k;
-  a.rows = (int32_t)rows, a.groups = groups, a.splits = wgrad_splits(rows, n, k, groups);
-  a.tiles_n = (uint32_t)((n + kWgTile - 1) / kWgTile), a.tiles_k = (uint32_t)((k + kWgTile - 1) / kWgTile);
-  a.total = (uint32_t)(wgrad_tiles(n, k, groups) * a.splits);
-  a.per_xcd = (a.total + 7) / 8;
-  const dim3 grid(a.per_xcd * 8), threads(kWgThreads);
-  const bool half = bf16 && a.splits == 1;
-  a.out = a.splits > 1 ? workspace : dw;
+  a.out = dw, a.part = workspace, a.rows = (int32_t)rows, a.groups = groups;
+  a.tiles_n = p.tiles_n, a.tiles_k = p.tiles_k, a.whole = p.whole, a.pieces = p.pieces, a.piece_stages = p.piece_stages;
+  const dim3 grid((unsigned)p.blocks), threads(kWgThreads);
   if (vec) {
-    if (half)
+    if (bf16)
       hipLaunchKernelGGL((wgrad_kernel<true, true>), grid, threads, 0, stream, a);
     else
       hipLaunchKernelGGL((wgrad_kernel<true, false>), grid, threads, 0, stream, a);
   } else {
-    if (half)
+    if (bf16)
       hipLaunchKernelGGL((wgrad_kernel<false, true>), grid, threads, 0, stream, a);
     else
       hipLaunchKernelGGL((wgrad_kernel<false, false>), grid, threads, 0, stream, a);
   }
   const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || a.splits == 1)
+  if (e != hipSuccess || p.cut == 0)
     return e;
-  const int64_t elems = groups * n * k;
-  const dim3 fold((unsigned)((elems / 4 + 255) / 256));
+  // several groups: most of these find that their group is not cut, so fewer
+  const int32_t fold_rows = groups == 1 ? 4 : 32;
+  const dim3 fold(kWgTile / fold_rows, groups == 1 ? p.cut : p.tiles_n * p.tiles_k, groups == 1 ? 1 : p.cut);
   if (bf16)
-    hipLaunchKernelGGL((wgrad_fold_kernel<true>), fold, dim3(256), 0, stream, workspace, a.splits, elems, dw);
+    hipLaunchKernelGGL((wgrad_fold_kernel<true>), fold, dim3(256), 0, stream, a, fold_rows);
   else
-    hipLaunchKernelGGL((wgrad_fold_kernel<false>), fold, dim3(256), 0, stream, workspace, a.splits, elems, dw);
+    hipLaunchKernelGGL((wgrad_fold_kernel<false>), fold, dim3(256), 0, stream, a, fold_rows);
   return hipGetLastError();
 }
 
