@@ -100,6 +100,8 @@ __device__ __forceinline__ void store(T* p, const float (&f)[N]) {
   } else {
     if constexpr (N == 1) {
       *p = (uint16_t)bf16_pair(f[0], f[0]);
+    } else if constexpr (N == 4) {
+      *reinterpret_cast<u32x2*>(p) = (u32x2){bf16_pair(f[0], f[1]), bf16_pair(f[2], f[3])};
     } else {
 #pragma unroll
       for (int i = 0; i < N; i += 8)

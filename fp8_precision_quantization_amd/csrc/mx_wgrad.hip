@@ -55,24 +55,32 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef u32x4 u32x4_any __attribute__((aligned(2)));
 
 constexpr int kWgThreads = 256;
-constexpr int kWgTile = 256;
 constexpr int kWgTokens = 64;                        // tokens per stage
-constexpr int kWgBlocks = 8;                         // 16 x 16 blocks per wave each way
-constexpr int kWgRow = kWgTile * 2;                  // bytes of a stage row of dy
-constexpr int kWgX = kWgTokens * kWgRow;             // where the codes start in a stage: rows of kWgTile bytes
-constexpr int kWgS = kWgX + kWgTokens * kWgTile;     // where the scales start: a dword each, [block of 32][token]
-constexpr int kWgScaleRow = 4 * kWgTokens + 16;      // (16 more than the banks' period)
-constexpr int kWgSlot = kWgS + kWgTile / MX_BLOCK * kWgScaleRow + 128;
-constexpr int kWgSlots = 3;
+constexpr int kWgSlots = 3;                          // stages in LDS
 constexpr int kWgCus = 256;
-static_assert(kWgSlot % 256 == 0 && kWgSlots * kWgSlot <= 160 * 1024, "stages fit LDS");
+constexpr int kWgScaleRow = 4 * kWgTokens + 16;      // a block's scales (16 bytes more than the banks' period)
+
+// Sizes of a tile of 32 NB x 32 NB: a wave has NB x NB blocks of 16 x 16.
+template <int NB>
+struct WgTile {
+  static constexpr int kTile = 32 * NB;
+  static constexpr int kRow = 2 * kTile;             // bytes of a stage row of dy
+  static constexpr int kX = kWgTokens * kRow;        // where the codes start in a stage: rows of kTile bytes
+  static constexpr int kS = kX + kWgTokens * kTile;  // where the scales start: a dword each, [block of 32][token]
+  static constexpr int kSlot = (kS + NB * kWgScaleRow + 255) / 256 * 256;
+  static constexpr int kPerCu = NB == 8 ? 1 : 2;     // workgroups
+  static constexpr int kLoadsDy = NB, kLoadsX = NB / 2, kLoadsS = NB / 4;   // a wave's to a stage
+  static constexpr int kLoads = kLoadsDy + kLoadsX + kLoadsS;
+  static_assert(NB == 4 || NB == 8, "tiles");
+  static_assert(kPerCu * kWgSlots * kSlot <= 160 * 1024, "stages fit LDS");
+};
 
 struct WgradArgs {
   const uint16_t* dy;
   const uint8_t *q, *s;
   const int32_t* ends;
   void* out;
-  float* part;        // sums of pieces, a 256 x 256 tile each
+  float* part;        // sums of pieces, a whole tile each
   int64_t lddy, n, k;
   int32_t rows, groups;
   uint32_t tiles_n, tiles_k;
@@ -222,9 +230,12 @@ __device__ __forceinline__ void wait_loads() {
   __builtin_amdgcn_s_waitcnt(0x0F70 | (N & 15) | (N >> 4 << 14));
 }
 
-template <bool VEC, bool BF16>
-__global__ __launch_bounds__(kWgThreads) __attribute__((amdgpu_waves_per_eu(1, 1))) void wgrad_kernel(WgradArgs a) {
-  __shared__ __attribute__((aligned(256))) uint8_t lds[kWgSlots * kWgSlot];
+template <int NB, bool VEC, bool BF16>
+__global__ __launch_bounds__(kWgThreads)
+    __attribute__((amdgpu_waves_per_eu(WgTile<NB>::kPerCu, WgTile<NB>::kPerCu))) void wgrad_kernel(WgradArgs a) {
+  using Tile = WgTile<NB>;
+  constexpr int kTile = Tile::kTile, kRow = Tile::kRow, kSlot = Tile::kSlot;
+  __shared__ __attribute__((aligned(256))) uint8_t lds[kWgSlots * kSlot];
   const uint32_t tiles = a.tiles_n * a.tiles_k;
   WgradItem it = {0, 0, a.rows, -1};
   int32_t tile;
@@ -257,7 +268,7 @@ __global__ __launch_bounds__(kWgThreads) __attribute__((amdgpu_waves_per_eu(1, 1
   // values that came through vector registers, made scalar
   const int32_t g = __builtin_amdgcn_readfirstlane(it.g), part = __builtin_amdgcn_readfirstlane(it.part);
   const int32_t lo = __builtin_amdgcn_readfirstlane(it.lo), hi = __builtin_amdgcn_readfirstlane(it.hi);
-  const int64_t i0 = (int64_t)((uint32_t)tile / a.tiles_k) * kWgTile, j0 = (int64_t)((uint32_t)tile % a.tiles_k) * kWgTile;
+  const int64_t i0 = (int64_t)((uint32_t)tile / a.tiles_k) * kTile, j0 = (int64_t)((uint32_t)tile % a.tiles_k) * kTile;
 
   const int t = threadIdx.x;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
@@ -265,57 +276,61 @@ __global__ __launch_bounds__(kWgThreads) __attribute__((amdgpu_waves_per_eu(1, 1
   const int wi = wave >> 1, wj = wave & 1;
   const int64_t ks = a.k / MX_BLOCK;
 
-  f32x4 acc[kWgBlocks][kWgBlocks];
+  f32x4 acc[NB][NB];
 #pragma unroll
-  for (int i = 0; i < kWgBlocks; ++i)
+  for (int i = 0; i < NB; ++i)
 #pragma unroll
-    for (int j = 0; j < kWgBlocks; ++j)
+    for (int j = 0; j < NB; ++j)
       acc[i][j] = (f32x4){};
 
-  // Loader roles, 14 loads of a wave to a stage.
-  //  dy: load u of wave w fills rows 8 u + 2 w, + 1; lane l the 16 bytes at
-  //  position l % 32 of row 8 u + 2 w + l / 32, whose source is chunk (l % 32)
-  //  ^ 2 f, f = row % 4 + 4 (row / 8 % 2).
-  //  codes: load u fills rows 16 u + 4 w .. + 3; lane l position l % 16 of row
-  //  16 u + 4 w + l / 16, source chunk (l % 16) ^ 8 (row / 8 % 2).
-  //  scales: loads of blocks 2 w, 2 w + 1; lane l is token l.
+  // Loader roles.  A load of a wave brings 1 KiB, whole rows of a stage:
+  //  dy: kDyRows rows; lane l the 16 bytes at position l % kDyLanes of its
+  //  row, whose source is chunk (l % kDyLanes) ^ 2 f, f = row % 4 + 4 (row / 8
+  //  % 2).
+  //  codes: kXRows rows; lane l position l % kXLanes of its row, whose source
+  //  is chunk (l % kXLanes) ^ kXLanes / 2 (row / 8 % 2).
+  //  scales: a block; lane l is token l.
+  constexpr int kDyLanes = kRow / 16, kDyRows = 64 / kDyLanes, kXLanes = kTile / 16, kXRows = 64 / kXLanes;
   const uint32_t lds0 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds);
-  const int drow = 2 * wave + lane / 32;
-  const int dchunk = (lane % 32) ^ (2 * (drow & 3));   // of even u; odd u: ^ 8
-  const int doff = drow * (int)a.lddy * 2 + 16 * dchunk, doff1 = drow * (int)a.lddy * 2 + 16 * (dchunk ^ 8);
-  const int xoff = (4 * wave + lane / 16) * (int)a.k + 16 * ((lane % 16) ^ (8 * (wave >> 1)));
-  const int soff = lane * (int)ks + 2 * wave;
+  const int drow = kDyRows * wave + lane / kDyLanes;   // of load 0; load u: + 4 kDyRows u
+  const int dchunk = (lane % kDyLanes) ^ (2 * (drow & 3)) ^ (drow & 8);
+  auto dchunk_of = [&](int u) { return dchunk ^ (4 * kDyRows * u & 8); };
+  const int doff = drow * (int)a.lddy * 2 + 16 * dchunk, doff1 = drow * (int)a.lddy * 2 + 16 * dchunk_of(1);
+  const int xrow = kXRows * wave + lane / kXLanes;     // load u: + 4 kXRows u, a multiple of 16
+  const int xoff = xrow * (int)a.k + 16 * ((lane % kXLanes) ^ (kXLanes / 2 * (xrow >> 3 & 1)));
+  const int soff = lane * (int)ks + Tile::kLoadsS * wave;
   const int64_t dy_end = (int64_t)(a.rows - 1) * a.lddy + a.n;   // elements of dy
-  u32x4 dreg[VEC ? 1 : 8];
+  u32x4 dreg[VEC ? 1 : Tile::kLoadsDy];
 
-  // The next stage to load, and load i of it (0 .. 13: eight of dy, four of
-  // codes, two of scales; without the first eight where dy goes through
-  // registers) into slot `slot`.  Past the last stage they load zeros.
+  // The next stage to load, and load i of it (dy, then codes, then scales;
+  // from kFirstLoad on where dy goes through registers) into slot `slot`.
+  // Past the last stage they load zeros.
   const int64_t tokens = hi - lo;
   Run run_dy = {reinterpret_cast<const uint8_t*>(a.dy + lo * a.lddy + i0), ((tokens - 1) * a.lddy + a.n - i0) * 2,
                 kWgTokens * a.lddy * 2};
   Run run_q = {a.q + lo * a.k + j0, tokens * a.k - j0, kWgTokens * a.k};
   Run run_s = {a.s + lo * ks + j0 / MX_BLOCK, tokens * ks - j0 / MX_BLOCK, kWgTokens * ks};
+  constexpr int kX0 = Tile::kLoadsDy, kS0 = kX0 + Tile::kLoadsX, kLoads = Tile::kLoads;
   auto target = [&](int i, int slot) {
-    const uint32_t to = lds0 + slot * kWgSlot;
-    lds_target(to + (i < 8    ? (8 * i + 2 * wave) * kWgRow
-                     : i < 12 ? kWgX + (16 * (i - 8) + 4 * wave) * kWgTile
-                              : kWgS + (2 * wave + i - 12) * kWgScaleRow));
+    const uint32_t to = lds0 + slot * kSlot;
+    lds_target(to + (i < kX0   ? (4 * i + wave) * kDyRows * kRow
+                     : i < kS0 ? Tile::kX + (4 * (i - kX0) + wave) * kXRows * kTile
+                               : Tile::kS + (Tile::kLoadsS * wave + i - kS0) * kWgScaleRow));
   };
   auto load = [&](int i) {
-    if (i < 8)
-      load_to_lds<16>(run_dy.rsrc(), (i % 2 ? doff1 : doff) + 8 * i * (int)a.lddy * 2);
-    else if (i < 12)
-      load_to_lds<16>(run_q.rsrc(), xoff + 16 * (i - 8) * (int)a.k);
+    if (i < kX0)
+      load_to_lds<16>(run_dy.rsrc(), (i % 2 ? doff1 : doff) + 4 * i * kDyRows * (int)a.lddy * 2);
+    else if (i < kS0)
+      load_to_lds<16>(run_q.rsrc(), xoff + 4 * (i - kX0) * kXRows * (int)a.k);
     else
-      load_to_lds<1>(run_s.rsrc(), soff + i - 12);
+      load_to_lds<1>(run_s.rsrc(), soff + i - kS0);
   };
   auto next_stage = [&]() {
     run_dy.next();
     run_q.next();
     run_s.next();
   };
-  constexpr int kFirstLoad = VEC ? 0 : 8, kStageLoads = 14 - kFirstLoad, kHalfLoads = kStageLoads / 2;
+  constexpr int kFirstLoad = VEC ? 0 : kX0, kStageLoads = kLoads - kFirstLoad, kHalfLoads = kStageLoads / 2;
   auto load_stage = [&](int slot, int loads) {
 #pragma unroll
     for (int i = kFirstLoad; i < kFirstLoad + loads; ++i) {
@@ -332,9 +347,9 @@ __global__ __launch_bounds__(kWgThreads) __attribute__((amdgpu_waves_per_eu(1, 1
       const int32_t m0 = lo + st * kWgTokens;
       const int32_t left = min(hi - m0, kWgTokens);
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        const int row = 8 * u + drow;
-        const int64_t c = i0 + 8 * (u % 2 ? dchunk ^ 8 : dchunk);
+      for (int u = 0; u < Tile::kLoadsDy; ++u) {
+        const int row = 4 * kDyRows * u + drow;
+        const int64_t c = i0 + 8 * dchunk_of(u);
         dreg[u] = (u32x4){0, 0, 0, 0};
         if (row < left && c < a.n) {
           const int64_t at = (int64_t)(m0 + row) * a.lddy + c;
@@ -351,8 +366,8 @@ __global__ __launch_bounds__(kWgThreads) __attribute__((amdgpu_waves_per_eu(1, 1
   auto put_dy = [&](int slot) {
     if constexpr (!VEC) {
 #pragma unroll
-      for (int u = 0; u < 8; ++u)
-        *reinterpret_cast<u32x4*>(lds + slot * kWgSlot + (8 * u + drow) * kWgRow + 16 * (lane % 32)) = dreg[u];
+      for (int u = 0; u < Tile::kLoadsDy; ++u)
+        *reinterpret_cast<u32x4*>(lds + slot * kSlot + (4 * kDyRows * u + drow) * kRow + 16 * (lane % kDyLanes)) = dreg[u];
     }
   };
 
@@ -361,106 +376,77 @@ __global__ __launch_bounds__(kWgThreads) __attribute__((amdgpu_waves_per_eu(1, 1
   const int l16 = lane & 15, lg = lane >> 4;
   const int tok = 8 * lg + (l16 >> 2);                        // dy reads: this token, and + 4
   const int swz = (tok & 3) | ((lg & 1) << 2);
-  const int a_at = tok * kWgRow + 256 * wi + 32 * swz + 8 * (lane & 3);   // block b at ^ 32 b
-  const int x_at = kWgX + 8 * lg * kWgTile + 128 * (wj ^ (lg & 1)) + 8 * l16;
-  const int s_at = kWgS + (4 * wj + l16 / 4) * kWgScaleRow + 32 * lg;
   typedef __attribute__((address_space(3))) s16x4* lds_s16x4;
-  typedef s16x4 Dy[kWgBlocks][2];   // a step's dy operands: 8 tokens of a column, in two reads
-  Dy d0, d1;
-  uint32_t x[kWgBlocks][4];         // a step's x operands
-  u32x2 codes[8];                   // 8 columns of each of 8 tokens
-  u32x4 scales[2];                  // those tokens' scale bytes
-
+  typedef s16x4 Dy[NB][2];              // a step's dy operands: 8 tokens of a column, in two reads
+  typedef uint32_t X[NB][4];            // ... and its x operands
+  struct Codes {
+    uint32_t q[8][NB / 4];              // NB columns of each of 8 tokens
+    u32x4 s[2];                         // those tokens' scale bytes
+  };
   // where the lane reads in the slot of the step that is read next
-  int d_at[kWgBlocks], x_from = x_at, s_from = s_at;
+  int d_at[NB];
 #pragma unroll
-  for (int i = 0; i < kWgBlocks; ++i)
-    d_at[i] = a_at ^ (32 * i);
-  auto read_dy = [&](int step, int r, Dy& d) {           // r: 0 .. 15
-    const uint8_t* p = lds + d_at[r / 2] + (32 * step + 4 * (r % 2)) * kWgRow;
+  for (int i = 0; i < NB; ++i)
+    d_at[i] = tok * kRow + 32 * ((NB * wi + i) ^ swz) + 8 * (lane & 3);
+  int x_at = Tile::kX + 8 * lg * kTile + kTile / 2 * (wj ^ (lg & 1)) + NB * l16;
+  int s_at = Tile::kS + (NB / 2 * wj + NB * l16 / 32) * kWgScaleRow + 32 * lg;
+  auto read_dy = [&](int step, int r, Dy& d) {                // r: 0 .. 2 NB - 1
+    const uint8_t* p = lds + d_at[r / 2] + (32 * step + 4 * (r % 2)) * kRow;
     d[r / 2][r % 2] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)p);
   };
-  auto read_x = [&](int step, int r) {                   // r: 0 .. 9, scales first
-    if (r < 2)
-      scales[r] = *reinterpret_cast<const u32x4*>(lds + s_from + 128 * step + 16 * r);
-    else
-      codes[r - 2] = *reinterpret_cast<const u32x2*>(lds + x_from + (32 * step + r - 2) * kWgTile);
+  auto read_scales = [&](int step, int r, Codes& c) {         // r: 0, 1
+    c.s[r] = *reinterpret_cast<const u32x4*>(lds + s_at + 128 * step + 16 * r);
   };
-  // Columns 2 c, 2 c + 1 of tokens 2 u, 2 u + 1: a dword of x blocks 2 c, 2 c
-  // + 1, in three parts of two instructions.
-  uint32_t pair[2];
-  auto convert = [&](int c, int u, int part) {
-    if (part < 2) {
-      const int t = 2 * u + part;
-      const float sc = __uint_as_float(scales[t / 4][t % 4] << 23);
-      pair[part] =
-          __builtin_bit_cast(uint32_t, c % 2 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes[t][c / 2], sc, true)
-                                             : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes[t][c / 2], sc, false));
+  auto read_codes = [&](int step, int r, Codes& c) {          // r: 0 .. 7
+    const uint8_t* p = lds + x_at + (32 * step + r) * kTile;
+    if constexpr (NB == 8) {
+      const u32x2 v = *reinterpret_cast<const u32x2*>(p);
+      c.q[r][0] = v[0], c.q[r][1] = v[1];
     } else {
-      x[2 * c][u] = __builtin_amdgcn_perm(pair[1], pair[0], 0x05040100u);
-      x[2 * c + 1][u] = __builtin_amdgcn_perm(pair[1], pair[0], 0x07060302u);
+      c.q[r][0] = *reinterpret_cast<const uint32_t*>(p);
     }
   };
-  auto convert_part = [&](int c, int i) { convert(c, i / 3, i % 3); };   // i: 0 .. 11
-  auto mfma = [&](int m, const Dy& d) {
-    const int i = m % kWgBlocks, j = m / kWgBlocks;
+  // Columns 2 p, 2 p + 1 of tokens 2 u, 2 u + 1: a dword of x blocks 2 p, 2 p
+  // + 1, in three parts of two instructions.
+  uint32_t pair[2];
+  auto convert = [&](int p, int u, int part, const Codes& c, X& x) {
+    if (part < 2) {
+      const int tk = 2 * u + part;
+      const float sc = __uint_as_float(c.s[tk / 4][tk % 4] << 23);
+      pair[part] =
+          __builtin_bit_cast(uint32_t, p % 2 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c.q[tk][p / 2], sc, true)
+                                             : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c.q[tk][p / 2], sc, false));
+    } else {
+      x[2 * p][u] = __builtin_amdgcn_perm(pair[1], pair[0], 0x05040100u);
+      x[2 * p + 1][u] = __builtin_amdgcn_perm(pair[1], pair[0], 0x07060302u);
+    }
+  };
+  auto mfma = [&](int m, const Dy& d, const X& x) {
+    const int i = m % NB, j = m / NB;
     const bf16x8 fa =
         __builtin_bit_cast(bf16x8, (s16x8)__builtin_shufflevector(d[i][0], d[i][1], 0, 1, 2, 3, 4, 5, 6, 7));
     const bf16x8 fb = __builtin_bit_cast(bf16x8, (u32x4){x[j][0], x[j][1], x[j][2], x[j][3]});
     // v_mfma_f32_16x16x32_bf16 with the accumulators tied to accumulation
-    // registers: given the intrinsic, the compiler moves the 64 of them about
-    // (428 register moves a stage).  Every operand was written at least four
-    // MFMAs earlier; the results are read after drain() below.
+    // registers: given the intrinsic, the compiler moves NB = 8's 64 of them
+    // about (428 register moves a stage).  Every operand was written at least
+    // one MFMA earlier; the results are read after the wait below the loop.
     asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(acc[i][j]) : "v"(fa), "v"(fb));
   };
 
-  // A stage is two steps of 32 tokens, 64 MFMAs each, x block after x block;
-  // there is one wave to a SIMD, so nothing but this order hides a wait.
-  // During a step the next step's codes and dy operands are read from LDS.
-  // The codes are converted in place, a pair of x blocks at a time once this
-  // step's MFMAs are through with it; the last pair follows at the beginning
-  // of the next step, and only then are the next codes read.
-  // Late in the first step of stage st the wave waits for its loads of stage
-  // st + 1 and meets the others at the stage's one barrier.  All of stage st
-  // has been read by then, and its slot takes the loads of stage st + 3.
-  // An MFMA takes 16 cycles, in which two or three other instructions issue:
-  // the rest is spread out accordingly, the loads (which queue up when they
-  // come together, and hold up the MFMAs behind them) one to eight MFMAs.
-  auto step = [&](int next, const Dy& now, Dy& then, auto first_c, int to) __attribute__((always_inline)) {
-    constexpr bool first = decltype(first_c)::value;
-    each(std::make_integer_sequence<int, kWgBlocks * kWgBlocks>(), [&](auto m_c) __attribute__((always_inline)) {
-      constexpr int m = decltype(m_c)::value;
-      constexpr int i = m % 8 == 1 && m / 8 < kHalfLoads ? kFirstLoad + m / 8 + (first ? kHalfLoads : 0) : 14;
-      if constexpr (i < 14)
-        target(i, to);
-      mfma(m, now);
-      if constexpr (i < 14)
-        load(i);
-      if constexpr (m < 12)
-        convert_part(3, m);
-      if constexpr (m >= 12 && m < 22)
-        read_x(next, m - 12);
-      if constexpr (m >= 22 && m < 28) {
-        read_dy(next, 2 * (m - 22), then);
-        read_dy(next, 2 * (m - 22) + 1, then);
-      }
-      if constexpr (m >= 28 && m < 32)
-        read_dy(next, m - 16, then);
-      if constexpr (m >= 28)
-        convert_part((m - 28) / 12, (m - 28) % 12);
-      if constexpr (m == 58) {
-        if (first) {
-          next_stage();
-          put_dy(to);   // where dy comes through registers
-          wait_loads<kStageLoads>();
-          lds_barrier();
-        }
-      }
-      __builtin_amdgcn_sched_barrier(0);
-    });
+  // A stage is two steps of 32 tokens, NB * NB MFMAs each, x block after x
+  // block.  In the first step of stage st the wave waits for its loads of
+  // stage st + 1 and meets the others at the stage's one barrier; all of stage
+  // st has been read by then, and its slot takes the loads of stage st + 3:
+  // half of them in the second step, half in the first of stage st + 1.
+  constexpr int kM = NB * NB;
+  auto arrive = [&](int to) {
+    next_stage();
+    put_dy(to);   // where dy comes through registers
+    wait_loads<kStageLoads>();
+    lds_barrier();
   };
-  if (hi > lo) {
-    const int stages = (hi - lo + kWgTokens - 1) / kWgTokens;
+  const int stages = (hi - lo + kWgTokens - 1) / kWgTokens;
+  if (stages > 0) {
     load_dy(0);
     put_dy(0);
     load_dy(1);
@@ -473,58 +459,171 @@ __global__ __launch_bounds__(kWgThreads) __attribute__((amdgpu_waves_per_eu(1, 1
     load_stage(2, kHalfLoads);
     wait_loads<kStageLoads + kHalfLoads>();   // stage 0 has landed
     lds_barrier();
+  }
+  int slot = 0, last = kWgSlots - 1;   // of this stage, of the one before
+  Dy d0, d1;
+  if constexpr (NB == 8) {
+    // One wave to a SIMD: nothing but this order hides a wait.  During a step
+    // the next step's codes and dy operands are read from LDS.  The codes are
+    // converted in place, a pair of x blocks at a time once this step's MFMAs
+    // are through with it; the last pair follows at the beginning of the next
+    // step, and only then are the next codes read.  An MFMA takes 16 cycles,
+    // in which two or three other instructions issue: the rest is spread out
+    // accordingly, the loads (which queue up when they come together, and hold
+    // up the MFMAs behind them) one to eight MFMAs.
+    X x;
+    Codes c;
+    auto step = [&](int next, const Dy& now, Dy& then, auto first_c, int to) __attribute__((always_inline)) {
+      constexpr bool first = decltype(first_c)::value;
+      each(std::make_integer_sequence<int, kM>(), [&](auto m_c) __attribute__((always_inline)) {
+        constexpr int m = decltype(m_c)::value;
+        constexpr int i = m % 8 == 1 && m / 8 < kHalfLoads ? kFirstLoad + m / 8 + (first ? kHalfLoads : 0) : kLoads;
+        if constexpr (i < kLoads)
+          target(i, to);
+        mfma(m, now, x);
+        if constexpr (i < kLoads)
+          load(i);
+        if constexpr (m < 12)
+          convert(3, m / 3, m % 3, c, x);
+        if constexpr (m >= 12 && m < 14)
+          read_scales(next, m - 12, c);
+        if constexpr (m >= 14 && m < 22)
+          read_codes(next, m - 14, c);
+        if constexpr (m >= 22 && m < 28) {
+          read_dy(next, 2 * (m - 22), then);
+          read_dy(next, 2 * (m - 22) + 1, then);
+        }
+        if constexpr (m >= 28 && m < 32)
+          read_dy(next, m - 16, then);
+        if constexpr (m >= 28)
+          convert((m - 28) / 12, (m - 28) % 12 / 3, m % 3 == 1 ? 0 : m % 3 == 2 ? 1 : 2, c, x);
+        if constexpr (m == 58 && first)
+          arrive(to);
+        __builtin_amdgcn_sched_barrier(0);
+      });
+    };
+    if (stages > 0) {
 #pragma unroll
-    for (int r = 0; r < 10; ++r)
-      read_x(0, r);
+      for (int r = 0; r < 2; ++r)
+        read_scales(0, r, c);
 #pragma unroll
-    for (int r = 0; r < 16; ++r)
-      read_dy(0, r, d0);
+      for (int r = 0; r < 8; ++r)
+        read_codes(0, r, c);
 #pragma unroll
-    for (int r = 0; r < 36; ++r)
-      convert_part(r / 12, r % 12);
-    int slot = 0;
+      for (int r = 0; r < 2 * NB; ++r)
+        read_dy(0, r, d0);
+#pragma unroll
+      for (int r = 0; r < 36; ++r)
+        convert(r / 12, r % 12 / 3, r % 3, c, x);
+    }
     for (int st = 0; st < stages; ++st) {
-      step(1, d0, d1, std::true_type(), slot == 0 ? kWgSlots - 1 : slot - 1);
+      const int next = slot + 1 == kWgSlots ? 0 : slot + 1, by = (next - slot) * kSlot;
+      step(1, d0, d1, std::true_type(), last);
       load_dy(st + 3);
-      const int to = slot + 1 == kWgSlots ? 0 : slot + 1;
-      const int by = (to - slot) * kWgSlot;
-      x_from += by;
-      s_from += by;
+      x_at += by;
+      s_at += by;
 #pragma unroll
-      for (int i = 0; i < kWgBlocks; ++i)
+      for (int i = 0; i < NB; ++i)
         d_at[i] += by;
       step(0, d1, d0, std::false_type(), slot);
-      slot = to;
+      last = slot;
+      slot = next;
     }
-    // loads into LDS still in flight must land before the workgroup ends
-    wait_loads<0>();
+  } else {
+    // Two waves to a SIMD.  During a step the next step's dy operands are read
+    // from LDS, its codes (read during the step before) are converted, and the
+    // codes of the step after it are read.
+    X x0, x1;
+    Codes c0, c1;
+    auto step = [&](int number, const Dy& d, const X& x, Dy& d_next, X& x_next, const Codes& c_next, Codes& c_then,
+                    auto first_c, int to, int by) __attribute__((always_inline)) {
+      constexpr bool first = decltype(first_c)::value;
+      each(std::make_integer_sequence<int, kM>(), [&](auto m_c) __attribute__((always_inline)) {
+        constexpr int m = decltype(m_c)::value;
+        constexpr int n = (first ? kHalfLoads : 0) + m / 3;
+        constexpr int i = m % 3 == 1 && n < (first ? kStageLoads : kHalfLoads) && m < 11 ? kFirstLoad + n : kLoads;
+        if constexpr (i < kLoads)
+          target(i, to);
+        mfma(m, d, x);
+        if constexpr (i < kLoads)
+          load(i);
+        if constexpr (m < 8)
+          read_dy(number ^ 1, m, d_next);
+        // 24 parts over 16 MFMAs
+        each(std::make_integer_sequence<int, m % 2 + 1>(), [&](auto e_c) {
+          constexpr int r = m / 2 * 3 + m % 2 + decltype(e_c)::value;
+          convert(r / 12, r % 12 / 3, r % 3, c_next, x_next);
+        });
+        if constexpr (m == 11 && first) {
+          arrive(to);
+          x_at += by;
+          s_at += by;
+        }
+        if constexpr (m >= 12) {
+          if constexpr (m < 14)
+            read_scales(number, m - 12, c_then);
+          read_codes(number, 2 * (m - 12), c_then);
+          read_codes(number, 2 * (m - 12) + 1, c_then);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      });
+    };
+    if (stages > 0) {
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        read_scales(0, r, c0);
+        read_scales(1, r, c1);
+      }
+#pragma unroll
+      for (int r = 0; r < 8; ++r) {
+        read_codes(0, r, c0);
+        read_codes(1, r, c1);
+        read_dy(0, r, d0);
+      }
+#pragma unroll
+      for (int r = 0; r < 24; ++r)
+        convert(r / 12, r % 12 / 3, r % 3, c0, x0);
+    }
+    for (int st = 0; st < stages; ++st) {
+      const int next = slot + 1 == kWgSlots ? 0 : slot + 1, by = (next - slot) * kSlot;
+      step(0, d0, x0, d1, x1, c1, c0, std::true_type(), last, by);
+      load_dy(st + 3);
+#pragma unroll
+      for (int i = 0; i < NB; ++i)
+        d_at[i] += by;
+      step(1, d1, x1, d0, x0, c0, c1, std::false_type(), slot, by);
+      last = slot;
+      slot = next;
+    }
   }
+  // loads into LDS still in flight must land before the workgroup ends
+  wait_loads<0>();
   // an MFMA's result may be read 18 cycles after it at the earliest
   asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
 #pragma unroll
-  for (int i = 0; i < kWgBlocks; ++i)
+  for (int i = 0; i < NB; ++i)
 #pragma unroll
-    for (int j = 0; j < kWgBlocks; ++j)
+    for (int j = 0; j < NB; ++j)
       asm volatile("" : "+a"(acc[i][j]));
 
-  // Register v of lane l: row 4 (l / 16) + v of its block; the lane's 8 blocks
-  // along k are 8 neighbouring columns.
-  const int64_t col = j0 + 128 * wj + 8 * l16;
+  // Register v of lane l: row 4 (l / 16) + v of its block; the lane's NB
+  // blocks along k are NB neighbouring columns.
+  const int64_t col = j0 + kTile / 2 * wj + NB * l16;
   if (part < 0 && col >= a.k)
     return;
   constexpr int kBytes = BF16 ? 2 : 4;
   const bool whole = (reinterpret_cast<uintptr_t>(a.out) & 15) == 0;
 #pragma unroll
-  for (int i = 0; i < kWgBlocks; ++i)
+  for (int i = 0; i < NB; ++i)
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
-      const int row = 128 * wi + 16 * i + 4 * lg + v;
-      float f[8];
+      const int row = kTile / 2 * wi + 16 * i + 4 * lg + v;
+      float f[NB];
 #pragma unroll
-      for (int j = 0; j < kWgBlocks; ++j)
+      for (int j = 0; j < NB; ++j)
         f[j] = acc[i][j][v];
       if (part >= 0) {
-        store(a.part + ((int64_t)part * kWgTile + row) * kWgTile + 128 * wj + 8 * l16, f);
+        store(a.part + ((int64_t)part * kTile + row) * kTile + kTile / 2 * wj + NB * l16, f);
         continue;
       }
       if (i0 + row >= a.n)
@@ -537,7 +636,7 @@ __global__ __launch_bounds__(kWgThreads) __attribute__((amdgpu_waves_per_eu(1, 1
           store(static_cast<float*>(at), f);
       } else {
 #pragma unroll
-        for (int j = 0; j < kWgBlocks; ++j) {
+        for (int j = 0; j < NB; ++j) {
           if constexpr (BF16)
             static_cast<uint16_t*>(at)[j] = (uint16_t)bf16_pair(f[j], 0.0f);
           else
@@ -548,10 +647,10 @@ __global__ __launch_bounds__(kWgThreads) __attribute__((amdgpu_waves_per_eu(1, 1
 }
 
 // The cut tiles: dw = the sum of a tile's pieces, in their order.  A
-// workgroup adds up `rows` rows of a tile, four at a time, a thread four
-// columns.
-template <bool BF16>
+// workgroup adds up `rows` rows of a tile, a thread four columns.
+template <int NB, bool BF16>
 __global__ __launch_bounds__(256) void wgrad_fold_kernel(WgradArgs a, int32_t rows) {
+  constexpr int kTile = 32 * NB, kAcross = kTile / 4, kDown = 256 / kAcross;
   const uint32_t tiles = a.tiles_n * a.tiles_k;
   int32_t g = 0, pieces = (int32_t)a.pieces;
   int64_t tile = blockIdx.y, part = blockIdx.y, stride = tiles - a.whole;   // first piece's part, parts from piece to piece
@@ -564,17 +663,18 @@ __global__ __launch_bounds__(256) void wgrad_fold_kernel(WgradArgs a, int32_t ro
     part += (int64_t)first_part * tiles;
     stride = tiles;
   }
-  const int64_t i0 = tile / a.tiles_k * kWgTile, j0 = tile % a.tiles_k * kWgTile;
-  const int col = (threadIdx.x & 63) * 4;
+  const int64_t i0 = tile / a.tiles_k * kTile, j0 = tile % a.tiles_k * kTile;
+  const int col = threadIdx.x % kAcross * 4;
   if (j0 + col >= a.k)
     return;
   const bool whole = (reinterpret_cast<uintptr_t>(a.out) & 15) == 0;
-  for (int row = blockIdx.x * rows + (threadIdx.x >> 6); row < (int)(blockIdx.x + 1) * rows && i0 + row < a.n; row += 4) {
-    const float* p = a.part + (part * kWgTile + row) * kWgTile + col;
+  for (int row = blockIdx.x * rows + threadIdx.x / kAcross; row < (int)(blockIdx.x + 1) * rows && i0 + row < a.n;
+       row += kDown) {
+    const float* p = a.part + (part * kTile + row) * kTile + col;
     f32x4 sum = *reinterpret_cast<const f32x4*>(p);
 #pragma unroll 8
     for (int s = 1; s < pieces; ++s)
-      sum += *reinterpret_cast<const f32x4*>(p + s * stride * kWgTile * kWgTile);
+      sum += *reinterpret_cast<const f32x4*>(p + s * stride * kTile * kTile);
     const int64_t at = ((int64_t)g * a.n + i0 + row) * a.k + j0 + col;
     if constexpr (BF16) {
       const u32x2 w = {bf16_pair(sum[0], sum[1]), bf16_pair(sum[2], sum[3])};
@@ -595,58 +695,122 @@ __global__ __launch_bounds__(256) void wgrad_fold_kernel(WgradArgs a, int32_t ro
 
 // How a call is cut up, from its sizes alone.
 struct WgradPlan {
+  int nb;
   uint32_t tiles_n, tiles_k, whole, pieces;
   int32_t piece_stages;
   int64_t blocks, parts;   // workgroups; tiles of pieces' sums
   uint32_t cut;            // one group: tiles that are cut; several: groups that may be
 };
 
-// One workgroup fills a CU, so tiles run in rounds of 256.  One group: full
-// rounds keep their tiles whole; what is left over is cut along the tokens
-// into as many pieces as fill a round, but no more than balances the time
-// saved with the traffic of the pieces' sums (about 1.3 us a stage against
-// 0.13 us a piece and tile: pieces = sqrt(10 stages / tiles)).
+// What a plan is weighed with, in us, measured on MI355X: a workgroup's start
+// and end, one stage of it, and one piece's sums written and added up.
+template <int NB>
+struct WgradCost;
+template <>
+struct WgradCost<8> {
+  static constexpr double kStart = 12.0, kStage = 1.4, kPart = 0.13;
+};
+template <>
+struct WgradCost<4> {
+  static constexpr double kStart = 5.0, kStage = 1.05, kPart = 0.033;
+};
+constexpr double kWgFold = 6.0;   // the kernel that adds pieces up, at least
+
+// Tiles run in rounds of as many as the GPU holds.  One group: full rounds
+// keep their tiles whole; what is left over is cut along the tokens into as
+// many pieces as fill a round, but no more than balances the time saved with
+// the traffic of the pieces' sums (the sum of stages / pieces and pieces *
+// tiles, each at its cost, is least at a square root).
 // Several groups: a group is cut where it is more than half as long again as
-// its share of the GPU (and of 24 stages); from eight rounds of tiles on, none.
-static WgradPlan wgrad_plan(int64_t rows, int64_t n, int64_t k, int32_t groups) {
+// its share of the GPU (and of 24 stages), if groups average 32 stages;
+// shorter ones cost more in pieces than they save.
+template <int NB>
+static WgradPlan wgrad_plan_of(int64_t rows, int64_t n, int64_t k, int32_t groups, double& cost) {
+  using Cost = WgradCost<NB>;
+  constexpr int64_t kRound = kWgCus * WgTile<NB>::kPerCu, kSide = WgTile<NB>::kTile;
   WgradPlan p = {};
-  p.tiles_n = (uint32_t)((n + kWgTile - 1) / kWgTile), p.tiles_k = (uint32_t)((k + kWgTile - 1) / kWgTile);
+  p.nb = NB;
+  p.tiles_n = (uint32_t)((n + kSide - 1) / kSide), p.tiles_k = (uint32_t)((k + kSide - 1) / kSide);
   const int64_t tiles = (int64_t)p.tiles_n * p.tiles_k;
   const int64_t stages = (rows + kWgTokens - 1) / kWgTokens;
   if (groups == 1) {
-    const int64_t cut = tiles % kWgCus;
+    const int64_t cut = tiles % kRound;
     int64_t pieces = 1;
     if (cut > 0) {
-      while ((pieces + 1) * (pieces + 1) * cut <= 10 * stages && (pieces + 1) * cut <= kWgCus && 2 * (pieces + 1) <= stages)
+      const double most = Cost::kStage * (double)stages / (Cost::kPart * (double)cut);
+      while ((double)((pieces + 1) * (pieces + 1)) <= most && (pieces + 1) * cut <= kRound && 2 * (pieces + 1) <= stages)
         ++pieces;
+      if (Cost::kStage * (double)(stages - stages / pieces) < kWgFold + Cost::kPart * (double)(pieces * cut))
+        pieces = 1;
     }
     p.cut = pieces > 1 ? (uint32_t)cut : 0;
     p.whole = (uint32_t)(tiles - p.cut), p.pieces = (uint32_t)pieces;
     p.parts = p.cut * pieces;
     p.blocks = segment_blocks(p.whole) + (int64_t)segment_blocks(p.cut) * pieces;
+    cost = (double)(tiles / kRound) * (Cost::kStart + Cost::kStage * (double)stages);
+    if (cut > 0)
+      cost += Cost::kStart + Cost::kStage * (double)((stages + pieces - 1) / pieces);
+    if (pieces > 1)
+      cost += kWgFold + Cost::kPart * (double)p.parts;
     return p;
   }
   const int64_t total = rows / kWgTokens + groups;   // at most: every group may end in a partial stage
-  int64_t each = INT32_MAX / 2;
-  if (tiles * groups < 8 * kWgCus) {
-    each = (total * tiles + kWgCus - 1) / kWgCus;
-    each = each < 24 ? 24 : each;
-  }
-  p.piece_stages = (int32_t)each;
-  p.pieces = (uint32_t)(total / each + groups);
-  const int64_t parts = total * 4 / (3 * each);      // a cut group is at least 1.5 pieces long
+  const int64_t share = (total * tiles + kRound - 1) / kRound, each = share < 24 ? 24 : share;
+  const bool may_cut = rows / kWgTokens >= 32 * (int64_t)groups && tiles * groups < 8 * kRound;
+  p.piece_stages = may_cut ? (int32_t)each : INT32_MAX / 2;
+  p.pieces = (uint32_t)(may_cut ? total / each + groups : groups);
+  const int64_t parts = may_cut ? total * 4 / (3 * each) : 0;   // a cut group is at least 1.5 pieces long
   p.cut = (uint32_t)(parts / 2);
   p.parts = p.cut > 0 ? parts * tiles : 0;
   p.blocks = (int64_t)segment_blocks((uint32_t)tiles) * p.pieces;
+  // groups of uneven length: the longest of few tiles to a CU sets the time
+  const double rounds = (double)(tiles * groups) / (double)kRound;
+  const double even = (double)total / (double)groups;
+  cost = (rounds < 1.0 ? 1.0 : rounds) * (Cost::kStart + Cost::kStage * even) + (rounds < 2.0 ? Cost::kStage * even : 0.0);
   return p;
 }
 
+// 256 x 256 tiles move half as much per product as 128 x 128 tiles and keep
+// the matrix cores busier (16640 x 4096 x 4096: 380 against 546 us); the
+// smaller ones start and end sooner, two to a CU, and there are four times as
+// many (1024 x 2048 x 2048: 16 against 29 us).
+static WgradPlan wgrad_plan(int64_t rows, int64_t n, int64_t k, int32_t groups) {
+  double cost8, cost4;
+  const WgradPlan p8 = wgrad_plan_of<8>(rows, n, k, groups, cost8);
+  const WgradPlan p4 = wgrad_plan_of<4>(rows, n, k, groups, cost4);
+#ifdef WG_NB
+  return WG_NB == 8 ? p8 : p4;
+#endif
+  return cost8 <= cost4 ? p8 : p4;
+}
+
 int64_t wgrad_workspace_bytes(int64_t rows, int64_t n, int64_t k, int32_t groups) {
-  return wgrad_plan(rows, n, k, groups).parts * kWgTile * kWgTile * 4;
+  const WgradPlan p = wgrad_plan(rows, n, k, groups);
+  return p.parts * (32 * p.nb) * (32 * p.nb) * 4;
 }
 
 int64_t wgrad_grid_blocks(int64_t rows, int64_t n, int64_t k, int32_t groups) {
   return wgrad_plan(rows, n, k, groups).blocks;
+}
+
+template <int NB, bool VEC, bool BF16>
+static hipError_t launch_wgrad_tile(const WgradArgs& a, const WgradPlan& p, hipStream_t stream) {
+  hipLaunchKernelGGL((wgrad_kernel<NB, VEC, BF16>), dim3((unsigned)p.blocks), dim3(kWgThreads), 0, stream, a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || p.cut == 0)
+    return e;
+  // several groups: most of these find that their group is not cut, so fewer
+  const int32_t rows = a.groups == 1 ? 32 / NB : 8 * NB;
+  const dim3 fold(32 * NB / rows, a.groups == 1 ? p.cut : p.tiles_n * p.tiles_k, a.groups == 1 ? 1 : p.cut);
+  hipLaunchKernelGGL((wgrad_fold_kernel<NB, BF16>), fold, dim3(256), 0, stream, a, rows);
+  return hipGetLastError();
+}
+
+template <int NB>
+static hipError_t launch_wgrad_any(const WgradArgs& a, const WgradPlan& p, bool vec, bool bf16, hipStream_t stream) {
+  if (vec)
+    return bf16 ? launch_wgrad_tile<NB, true, true>(a, p, stream) : launch_wgrad_tile<NB, true, false>(a, p, stream);
+  return bf16 ? launch_wgrad_tile<NB, false, true>(a, p, stream) : launch_wgrad_tile<NB, false, false>(a, p, stream);
 }
 
 hipError_t launch_wgrad(const void* dy, int64_t lddy, const uint8_t* q, const uint8_t* s, int64_t rows, int64_t n,
@@ -657,29 +821,7 @@ hipError_t launch_wgrad(const void* dy, int64_t lddy, const uint8_t* q, const ui
   a.dy = static_cast<const uint16_t*>(dy), a.lddy = lddy, a.q = q, a.s = s, a.ends = ends, a.n = n, a.k = k;
   a.out = dw, a.part = workspace, a.rows = (int32_t)rows, a.groups = groups;
   a.tiles_n = p.tiles_n, a.tiles_k = p.tiles_k, a.whole = p.whole, a.pieces = p.pieces, a.piece_stages = p.piece_stages;
-  const dim3 grid((unsigned)p.blocks), threads(kWgThreads);
-  if (vec) {
-    if (bf16)
-      hipLaunchKernelGGL((wgrad_kernel<true, true>), grid, threads, 0, stream, a);
-    else
-      hipLaunchKernelGGL((wgrad_kernel<true, false>), grid, threads, 0, stream, a);
-  } else {
-    if (bf16)
-      hipLaunchKernelGGL((wgrad_kernel<false, true>), grid, threads, 0, stream, a);
-    else
-      hipLaunchKernelGGL((wgrad_kernel<false, false>), grid, threads, 0, stream, a);
-  }
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || p.cut == 0)
-    return e;
-  // several groups: most of these find that their group is not cut, so fewer
-  const int32_t fold_rows = groups == 1 ? 4 : 32;
-  const dim3 fold(kWgTile / fold_rows, groups == 1 ? p.cut : p.tiles_n * p.tiles_k, groups == 1 ? 1 : p.cut);
-  if (bf16)
-    hipLaunchKernelGGL((wgrad_fold_kernel<true>), fold, dim3(256), 0, stream, a, fold_rows);
-  else
-    hipLaunchKernelGGL((wgrad_fold_kernel<false>), fold, dim3(256), 0, stream, a, fold_rows);
-  return hipGetLastError();
+  return p.nb == 8 ? launch_wgrad_any<8>(a, p, vec, bf16, stream) : launch_wgrad_any<4>(a, p, vec, bf16, stream);
 }
 
 }  // namespace mx

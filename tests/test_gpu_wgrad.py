@@ -184,3 +184,37 @@ def test_refusals():
                  lambda: mx.mx_wgrad_checkpoint(dy.t(), q, s)):
         with pytest.raises(ValueError):
             call()
+
+
+# larger outputs, both tile sizes: whole rounds, cut tiles, whole and cut ones
+# together, groups that are cut and that are not; aligned and odd widths
+LARGE = [(3000, 3104, 3104, None), (3000, 3101, 3104, None), (16640, 2048, 2048, None), (16640, 2047, 2048, None),
+         (1664, 4128, 4128, None), (1664, 4121, 4128, None), (5000, 5120, 4352, None), (5000, 5119, 4352, None),
+         (700, 3100, 3104, None), (2500, 2600, 2592, None), (500, 4096, 4096, [10, 300, 500]),
+         (16640, 3000, 4096, [100, 14000, 14100, 16640]), (16640, 2999, 4096, [15000, 15000, 16000, 16600]),
+         (6500, 600, 544, [6000, 6500]), (6500, 601, 544, [300, 6400])]
+
+
+@pytest.mark.parametrize("rows,n,k,ends", LARGE)
+def test_large_outputs(rows, n, k, ends):
+    """Against products in binary64 on the GPU."""
+    dev = device()
+    gen = torch.Generator(device=dev).manual_seed(rows + n + k)
+    dy = torch.randn(rows, n, device=dev, generator=gen).bfloat16()
+    q = (torch.randn(rows, k, device=dev, generator=gen) * 60).clamp(-448, 448).to(torch.float8_e4m3fn)
+    s = torch.randint(118, 130, (rows, k // 32), device=dev, generator=gen, dtype=torch.uint8)
+    x = q.double().view(rows, k // 32, 32) * torch.ldexp(torch.ones((), dtype=torch.float64, device=dev), s.int() - 127)[:, :, None]
+    x = x.view(rows, k)
+    e = None if ends is None else torch.tensor(ends, dtype=torch.int32, device=dev)
+    for dtype in (torch.float32, torch.bfloat16):
+        got = mx.mx_wgrad_checkpoint(dy, q, s, e, out_dtype=dtype)
+        lo = 0
+        for g, hi in enumerate([rows] if ends is None else ends):
+            a, b = dy[lo:hi].double(), x[lo:hi]
+            want, mag = a.t().contiguous() @ b, a.abs().t().contiguous() @ b.abs()
+            tol = (hi - lo + 32) * 2.0 ** -23 * mag
+            if dtype == torch.bfloat16:
+                tol += torch.exp2(torch.floor(torch.log2((want.abs() + tol).clamp(min=2.0 ** -126))) - 8)
+            off = ((got if ends is None else got[g]).double() - want).abs()
+            assert bool((off <= tol).all()), (dtype, g, int((off > tol).sum()))
+            lo = hi
