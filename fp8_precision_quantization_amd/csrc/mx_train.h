@@ -116,7 +116,7 @@ __device__ __forceinline__ void store(T* p, const float (&f)[N]) {
 template <int STEP>
 __device__ __forceinline__ uint32_t row16_move(uint32_t v) {
   constexpr int ctrl = STEP == 0 ? 0xB1 : STEP == 1 ? 0x4E : STEP == 2 ? 0x141 : 0x140;
-  return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, ctrl, 0xF, 0xF, false);
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, ctrl, 0xF, 0xF, true);
 }
 
 // op over the G lanes (16 or 64, aligned) a lane belongs to; every lane gets
@@ -153,9 +153,20 @@ __device__ __forceinline__ uint32_t lanes_min(uint32_t v) {
   return lanes_reduce<G>(v, [](uint32_t a, uint32_t b) { return min(a, b); });
 }
 
+// NaN if any is one (the maximum that keeps NaN).
+template <int G>
+__device__ __forceinline__ float lanes_fmax(float v) {
+  return __uint_as_float(lanes_reduce<G>(__float_as_uint(v), [](uint32_t x, uint32_t y) {
+    const float a = __uint_as_float(x), b = __uint_as_float(y);
+    return __float_as_uint(__builtin_elementwise_maximum(a, b));
+  }));
+}
+
+constexpr float kLog2E = 1.44269504088896341f;
+
 // e^x from the hardware's 2^x: the product with log2(e) is rounded once, so
 // the relative error grows like |x| * 2^-24, on top of the one or two ulp of
 // v_exp_f32.
-__device__ __forceinline__ float exp_fast(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504088896341f); }
+__device__ __forceinline__ float exp_fast(float x) { return __builtin_amdgcn_exp2f(x * kLog2E); }
 
 }  // namespace mx
