@@ -409,9 +409,23 @@ __global__ __launch_bounds__(kRouterBwdThreads) void router_bwd_kernel(RouterArg
   constexpr int kRows = 64 / G;
   constexpr int kWaves = kRouterBwdThreads / 64;
   constexpr int kKeep = (MX_MAX_TOPK + G - 1) / G;
+  // The chosen experts' d_j of the wave's rows, 0 elsewhere, W of a lane's
+  // logits side by side: the lanes that have them put them in, the lanes that
+  // own the columns take them out (comparing each column with each choice
+  // instead took 37 against 30 us for 65536 rows of 256, topk 8).
+  constexpr int W = V < 4 ? V : 4;
+  __shared__ __attribute__((aligned(16))) float sparse[kWaves][V / W][64][W];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lane = threadIdx.x & 63;
   const int gl = lane % G;
+  // place of column e of this lane's row
+  auto sparse_at = [&](int e) -> float& {
+    const int q = e / U, v = q / G * U + e % U;
+    return sparse[wave][v / W][lane / G * G + q % G][v % W];
+  };
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+    sparse[wave][v / W][lane][v % W] = 0.0f;
   const float dloss = a.dloss != nullptr ? *a.dloss : 0.0f;
   float bal[V];
 #pragma unroll
@@ -475,19 +489,22 @@ __global__ __launch_bounds__(kRouterBwdThreads) void router_bwd_kernel(RouterArg
     }
     along = lanes_sum<G>(along);
     if (a.dgates != nullptr) {
-      for (int j = 0; j < a.topk; ++j) {
-        int32_t e = -1;
-        float dj = 0.0f;
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
 #pragma unroll
-        for (int i = 0; i < kKeep; ++i)
-          if (i == j / G) {
-            e = __shfl(idx[i], j % G, G);
-            dj = __shfl(d[i], j % G, G);
-          }
+      for (int i = 0; i < kKeep; ++i)
+        if (idx[i] >= 0)
+          sparse_at(idx[i]) = d[i];
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+      __builtin_amdgcn_wave_barrier();
 #pragma unroll
-        for (int v = 0; v < V; ++v)
-          dp[v] += router_col<G, U>(v, gl) == e ? dj : 0.0f;
-      }
+      for (int v = 0; v < V; ++v)
+        dp[v] += sparse[wave][v / W][lane][v % W];
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+      __builtin_amdgcn_wave_barrier();
+#pragma unroll
+      for (int i = 0; i < kKeep; ++i)
+        if (idx[i] >= 0)
+          sparse_at(idx[i]) = 0.0f;
     }
     if (in) {
       T* dr = static_cast<T*>(a.dz) + row * a.experts;
