@@ -403,6 +403,10 @@ __global__ __launch_bounds__(kRouterThreads) void router_fold_kernel(RouterArgs 
 }
 
 constexpr int kRouterBwdThreads = 256;
+// Four workgroups to a CU, which go on to further rows: each sets up balance
+// and its LDS once.  65536 rows of 256: 256 workgroups 44 us, 512 32, 1024 30,
+// 2048 36, 4096 41.
+constexpr int64_t kRouterBwdBlocks = 1024;
 
 template <typename T, int G, int V, int U>
 __global__ __launch_bounds__(kRouterBwdThreads) void router_bwd_kernel(RouterArgs a) {
@@ -434,41 +438,58 @@ __global__ __launch_bounds__(kRouterBwdThreads) void router_bwd_kernel(RouterArg
     bal[v] = c < a.experts ? dloss * a.in_balance[c] : 0.0f;
   }
   const int64_t stride = (int64_t)gridDim.x * kWaves * kRows;
-  for (int64_t base = ((int64_t)blockIdx.x * kWaves + wave) * kRows; base < a.rows; base += stride) {
+  const int64_t start = ((int64_t)blockIdx.x * kWaves + wave) * kRows;
+  // the choices of the next rows, loaded a turn ahead: what they point at can
+  // then be loaded together with everything else
+  int32_t ahead[kKeep];
+  auto load_chosen = [&](int64_t row) {
+#pragma unroll
+    for (int i = 0; i < kKeep; ++i)
+      ahead[i] = row < a.rows && i * G + gl < a.topk ? a.in_chosen[row * a.topk + i * G + gl] : -1;
+  };
+  load_chosen(start + lane / G);
+  for (int64_t base = start; base < a.rows; base += stride) {
     const int64_t row = base + lane / G;
     const bool in = row < a.rows;
-    const bool part = in && a.in_chosen[row * a.topk] >= 0;
-    const T* zr = static_cast<const T*>(a.z) + (part ? row : 0) * a.ld;
-    const float lse = part ? a.in_lse[row] : 0.0f;
-    float z[V];
-    load_logits<T, G, V, U>(zr, part ? a.experts : 0, gl, -INFINITY, z);
-    float p[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-      p[v] = exp_fast(z[v] - lse);
-
     // lane j of the group works out d_j, d_{j + G}, ... of the chosen experts
     int32_t idx[kKeep];
     float d[kKeep], pc[kKeep], dg = 0.0f, total = 0.0f;
 #pragma unroll
+    for (int i = 0; i < kKeep; ++i)
+      idx[i] = ahead[i] < a.experts ? ahead[i] : -1;
+    // a row that takes no part has -1 in its first slot (of the group's first
+    // lane); what its logits hold is not used
+    const bool part = __shfl(ahead[0], 0, G) >= 0;
+    const T* zr = static_cast<const T*>(a.z) + (in ? row : 0) * a.ld;
+    const float lse = in ? a.in_lse[row] : 0.0f;
+    float z[V];
+    load_logits<T, G, V, U>(zr, in ? a.experts : 0, gl, -INFINITY, z);
+    float zc[kKeep], gate[kKeep];
+#pragma unroll
     for (int i = 0; i < kKeep; ++i) {
-      const int j = i * G + gl;
-      idx[i] = -1;
-      d[i] = pc[i] = 0.0f;
-      if (part && j < a.topk) {
-        const int32_t e = a.in_chosen[row * a.topk + j];
-        if (e >= 0 && e < a.experts) {
-          idx[i] = e;
-          float f[1];
-          unpack(zr + e, f);
-          pc[i] = exp_fast(f[0] - lse);
-          if (a.dgates != nullptr) {
-            d[i] = a.dgates[row * a.topk + j];
-            dg += d[i] * a.in_gates[row * a.topk + j];
-          }
-          total += pc[i];
+      d[i] = gate[i] = 0.0f;
+      zc[i] = -INFINITY;
+      if (idx[i] >= 0) {
+        const int64_t at = row * a.topk + i * G + gl;
+        float f[1];
+        unpack(zr + idx[i], f);
+        zc[i] = f[0];
+        if (a.dgates != nullptr) {
+          d[i] = a.dgates[at];
+          gate[i] = a.in_gates[at];
         }
       }
+    }
+    load_chosen(row + stride);
+    float p[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      p[v] = part ? exp_fast(z[v] - lse) : 0.0f;
+#pragma unroll
+    for (int i = 0; i < kKeep; ++i) {
+      pc[i] = exp_fast(zc[i] - lse);
+      dg += d[i] * gate[i];
+      total += pc[i];
     }
     if (a.normalize) {
       dg = lanes_sum<G>(dg);
@@ -611,7 +632,7 @@ hipError_t launch_router_bwd(const void* logits, int64_t ld, bool f32, const flo
   a.dloss = dloss, a.dz = dlogits;
   const int64_t per = router_rows_per_block(experts, kRouterBwdThreads / 64);
   const int64_t want = (rows + per - 1) / per;
-  return launch_router_any(a, f32, vec, true, want < 2048 ? want : 2048, stream);
+  return launch_router_any(a, f32, vec, true, want < kRouterBwdBlocks ? want : kRouterBwdBlocks, stream);
 }
 
 }  // namespace mx
