@@ -12,7 +12,7 @@
 // are in flight meanwhile.
 //
 // A row belongs to a team of WPR waves: one wave (four teams to a workgroup,
-// no barrier) or a whole workgroup (sums meet in LDS, one barrier each).  A
+// no barrier) or four and more (sums meet in LDS, one barrier each).  A
 // lane holds NCH chunks of VEC elements; chunk c of a row sits in lane c % 64
 // of wave (c / 64) % WPR, so a wave's load covers consecutive memory.  VEC is
 // 16 bytes, or one element where a pointer, the row length or the row pitch
@@ -39,7 +39,7 @@ struct NormArgs {
   float *mean, *rstd;
   uint8_t *q, *s;
   float* part;   // backward: a row of dw sums and one of db sums per workgroup
-  int32_t has_db;
+  float *dw, *db;
 };
 
 constexpr int norm_threads(int wpr) { return wpr == 1 ? 256 : 64 * wpr; }
@@ -63,7 +63,7 @@ __device__ __forceinline__ f32x2 team_sum(f32x2 v, f32x2 (&slots)[2][WPR], int& 
   v[1] = lanes_sum(v[1]);
   if constexpr (WPR > 1) {
     if ((threadIdx.x & 63) == 0)
-      slots[turn][threadIdx.x >> 6] = v;
+      slots[turn][(threadIdx.x >> 6) % WPR] = v;
     lds_barrier();
     v = slots[turn][0];
 #pragma unroll
@@ -76,6 +76,15 @@ __device__ __forceinline__ f32x2 team_sum(f32x2 v, f32x2 (&slots)[2][WPR], int& 
   return v;
 }
 
+// The range of a row, or an empty one: loads past it read zeros, stores past
+// it are dropped, so that rows and their ends need no branches.
+template <typename T>
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t row_range(const void* base, int64_t ld, int64_t row, int64_t rows,
+                                                            int32_t cols) {
+  const bool on = row < rows;
+  return buffer_rsrc(static_cast<const T*>(base) + (on ? row : 0) * ld, on ? (uint32_t)(cols * (int)sizeof(T)) : 0u);
+}
+
 template <typename T, int VEC, int WPR, int NCH, bool CKPT>
 __global__ __launch_bounds__(norm_threads(WPR)) void norm_fwd_kernel(NormArgs a) {
   constexpr int kTeams = WPR == 1 ? 4 : 1;
@@ -84,9 +93,7 @@ __global__ __launch_bounds__(norm_threads(WPR)) void norm_fwd_kernel(NormArgs a)
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lane = threadIdx.x & 63;
   const int first = ((WPR == 1 ? 0 : wave) * 64 + lane) * VEC;
-  constexpr int kStep = WPR * 64 * VEC;
-  const T* x = static_cast<const T*>(a.x);
-  T* y = static_cast<T*>(a.out);
+  constexpr int kStep = WPR * 64 * VEC, kBytes = sizeof(T);
 
   float w[NCH][VEC], b[NCH][VEC];
 #pragma unroll
@@ -105,15 +112,13 @@ __global__ __launch_bounds__(norm_threads(WPR)) void norm_fwd_kernel(NormArgs a)
   const int64_t stride = (int64_t)gridDim.x * kTeams;
   int64_t row = (int64_t)blockIdx.x * kTeams + (WPR == 1 ? wave : 0);
   Raw<T, VEC> raw[NCH];
+  auto load_row = [&](int64_t r) {
+    const __amdgpu_buffer_rsrc_t xs = row_range<T>(a.x, a.ldx, r, a.rows, a.cols);
 #pragma unroll
-  for (int j = 0; j < NCH; ++j) {
-    raw[j].clear();
-    const int c = first + j * kStep;
-    if (row < a.rows && c < a.cols)
-      raw[j].load(x + row * a.ldx + c);
-  }
-  // divided by, not multiplied with its reciprocal: a constant row's mean is
-  // then the constant itself
+    for (int j = 0; j < NCH; ++j)
+      raw[j].load(xs, (first + j * kStep) * kBytes);
+  };
+  load_row(row);
   const float cols = (float)a.cols;
   for (; row < a.rows; row += stride) {
     float v[NCH][VEC];
@@ -128,16 +133,12 @@ __global__ __launch_bounds__(norm_threads(WPR)) void norm_fwd_kernel(NormArgs a)
       }
       sum += part;
     }
-    // the next row's loads, in flight while this one is worked on
-    if (row + stride < a.rows) {
-      const T* xn = x + (row + stride) * a.ldx;
-#pragma unroll
-      for (int j = 0; j < NCH; ++j) {
-        const int c = first + j * kStep;
-        if (c < a.cols)
-          raw[j].load(xn + c);
-      }
-    }
+    // the next row's loads, in flight while this one is worked on; not before
+    // this row has left the registers they go to
+    __builtin_amdgcn_sched_barrier(0);
+    load_row(row + stride);
+    // divided by, not multiplied with the reciprocal: a constant row's mean is
+    // then the constant itself
     const float mean = team_sum<WPR>((f32x2){sum, 0.0f}, slots, turn)[0] / cols;
     float sq = 0.0f;
 #pragma unroll
@@ -148,8 +149,7 @@ __global__ __launch_bounds__(norm_threads(WPR)) void norm_fwd_kernel(NormArgs a)
         v[j][i] -= mean;
         part += v[j][i] * v[j][i];
       }
-      if (first + j * kStep < a.cols)
-        sq += part;
+      sq += first + j * kStep < a.cols ? part : 0.0f;
     }
     const float var = team_sum<WPR>((f32x2){sq, 0.0f}, slots, turn)[0] / cols;
     const float rstd = 1.0f / sqrtf(var + a.eps);
@@ -157,10 +157,9 @@ __global__ __launch_bounds__(norm_threads(WPR)) void norm_fwd_kernel(NormArgs a)
       a.mean[row] = mean;
       a.rstd[row] = rstd;
     }
-    T* yr = y + row * a.cols;
+    const __amdgpu_buffer_rsrc_t ys = row_range<T>(a.out, a.cols, row, a.rows, a.cols);
 #pragma unroll
     for (int j = 0; j < NCH; ++j) {
-      const int c = first + j * kStep;
 #pragma unroll
       for (int i = 0; i < VEC; ++i)
         v[j][i] = v[j][i] * rstd * w[j][i] + b[j][i];
@@ -175,34 +174,55 @@ __global__ __launch_bounds__(norm_threads(WPR)) void norm_fwd_kernel(NormArgs a)
         m = max2(m, quad_swap1(m));
         m = max2(m, quad_swap2(m));
         m = max(m & 0xFFFFu, m >> 16);
-        if (c < a.cols) {
-          const BlockParams p = block_params<true>(m);
-          const uint32_t c0 = quant4<true>(d[0], d[1], p), c1 = quant4<true>(d[2], d[3], p);
-          *reinterpret_cast<u32x4*>(yr + c) = (u32x4){d[0], d[1], d[2], d[3]};
-          *reinterpret_cast<u32x2*>(a.q + row * a.cols + c) = (u32x2){c0, c1};
-          if ((lane & 3) == 0)
-            a.s[row * (a.cols / MX_BLOCK) + c / MX_BLOCK] = (uint8_t)p.byte;
+        BlockParams p;
+        u32x2 c;
+        // a wave without infinities and NaN, as nearly all are, skips their cases
+        if (__any(m >= kInfBits)) {
+          p = block_params<true>(m);
+          c = (u32x2){quant4<true>(d[0], d[1], p), quant4<true>(d[2], d[3], p)};
+        } else {
+          p = block_params<false>(m);
+          c = (u32x2){quant4<false>(d[0], d[1], p), quant4<false>(d[2], d[3], p)};
         }
-      } else if (c < a.cols) {
-        store(yr + c, v[j]);
+        const __amdgpu_buffer_rsrc_t qs = buffer_rsrc(a.q + row * a.cols, (uint32_t)a.cols);
+        const __amdgpu_buffer_rsrc_t ss = buffer_rsrc(a.s + row * (a.cols / MX_BLOCK), (uint32_t)(a.cols / MX_BLOCK));
+        __builtin_amdgcn_raw_buffer_store_b128((u32x4){d[0], d[1], d[2], d[3]}, ys, (first + j * kStep) * kBytes, 0,
+                                               kCacheNT);
+        __builtin_amdgcn_raw_buffer_store_b64(c, qs, first + j * kStep, 0, kCacheNT);
+        // one lane of a block; the others' byte goes past the range
+        __builtin_amdgcn_raw_buffer_store_b8((char)p.byte, ss, (lane & 3) == 0 ? (first + j * kStep) / MX_BLOCK : 1 << 30,
+                                             0, 0);
+      } else {
+        store<T, kCacheNT>(ys, (first + j * kStep) * kBytes, v[j]);
       }
     }
   }
 }
 
+// Teams of a workgroup of the backward pass, and the most workgroups.  Each
+// workgroup leaves a row of dw sums and one of db sums to be added up
+// afterwards, so there are no more than keep the memory busy: one to a CU
+// where a workgroup is eight waves or more, two where it is four.  Two teams
+// of four waves with one workgroup to a CU halve those rows against one team
+// with two (16640 x 5120 bf16 107 -> 97 us); single elements have too few
+// bytes in flight for that (16640 x 1111 bf16: 44 and 62 us).
+constexpr int norm_bwd_teams(int wpr, int vec) { return wpr == 1 ? 4 : wpr == 4 && vec > 1 ? 2 : 1; }
+constexpr int64_t kBwdBlocks = 512;
+constexpr int64_t norm_bwd_blocks(int wpr, int vec) {
+  return wpr * norm_bwd_teams(wpr, vec) == 4 || vec == 1 ? kBwdBlocks : kBwdBlocks / 2;
+}
+
 template <typename T, int VEC, int WPR, int NCH>
-__global__ __launch_bounds__(norm_threads(WPR)) void norm_bwd_kernel(NormArgs a) {
-  constexpr int kTeams = WPR == 1 ? 4 : 1;
-  __shared__ f32x2 slots[2][WPR];
-  __shared__ f32x2 meet[kTeams == 1 ? 1 : 64 * NCH * VEC];   // dw, db of a one-wave team's columns
+__global__ __launch_bounds__(64 * WPR * norm_bwd_teams(WPR, VEC)) void norm_bwd_kernel(NormArgs a) {
+  constexpr int kTeams = norm_bwd_teams(WPR, VEC);
+  __shared__ f32x2 slots[kTeams][2][WPR];
+  __shared__ f32x2 meet[kTeams == 1 ? 1 : 64 * WPR * NCH * VEC];   // a team's dw and db sums
   int turn = 0;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lane = threadIdx.x & 63;
-  const int first = ((WPR == 1 ? 0 : wave) * 64 + lane) * VEC;
-  constexpr int kStep = WPR * 64 * VEC;
-  const T* x = static_cast<const T*>(a.x);
-  const T* dy = static_cast<const T*>(a.dy);
-  T* dx = static_cast<T*>(a.out);
+  const int team = wave / WPR;
+  const int first = (wave % WPR * 64 + lane) * VEC;
+  constexpr int kStep = WPR * 64 * VEC, kBytes = sizeof(T);
 
   float w[NCH][VEC], dw[NCH][VEC], db[NCH][VEC];
 #pragma unroll
@@ -216,43 +236,43 @@ __global__ __launch_bounds__(norm_threads(WPR)) void norm_bwd_kernel(NormArgs a)
   }
 
   const int64_t stride = (int64_t)gridDim.x * kTeams;
-  int64_t row = (int64_t)blockIdx.x * kTeams + (WPR == 1 ? wave : 0);
-  Raw<T, VEC> rx[NCH], rd[NCH];
-  float mean = 0.0f, rstd = 0.0f;
-#pragma unroll
-  for (int j = 0; j < NCH; ++j) {
-    rx[j].clear();
-    rd[j].clear();
-  }
+  int64_t row = (int64_t)blockIdx.x * kTeams + team;
+  // Reads past the caches and stores through them: 16640 x 8192 bf16 161 -> 150
+  // us, 16640 x 4096 binary32 153 -> 141 us.  Rows of one wave lose
+  // by it (16640 x 384: 13.9 -> 17.4 us), and so do single elements (16640 x
+  // 1111 bf16: 44 -> 72 us), whose stores need the cache to be joined.
+  constexpr int kInPolicy = VEC > 1 && WPR > 1 ? kCacheNT : 0;
+  constexpr int kDxPolicy = kInPolicy == 0 ? kCacheNT : kCacheThrough;
+  Raw<T, VEC, kInPolicy> rx[NCH], rd[NCH];
+  Raw<float, 1> rm, rr;
   auto load_row = [&](int64_t r) {
-    const T* xn = x + r * a.ldx;
-    const T* dn = dy + r * a.lddy;
-    mean = a.mean[r];
-    rstd = a.rstd[r];
+    const __amdgpu_buffer_rsrc_t xs = row_range<T>(a.x, a.ldx, r, a.rows, a.cols);
+    const __amdgpu_buffer_rsrc_t ds = row_range<T>(a.dy, a.lddy, r, a.rows, a.cols);
+    rm.load(row_range<float>(a.mean, 1, r, a.rows, 1), 0);
+    rr.load(row_range<float>(a.rstd, 1, r, a.rows, 1), 0);
 #pragma unroll
     for (int j = 0; j < NCH; ++j) {
-      const int c = first + j * kStep;
-      if (c < a.cols) {
-        rx[j].load(xn + c);
-        rd[j].load(dn + c);
-      }
+      rx[j].load(xs, (first + j * kStep) * kBytes);
+      rd[j].load(ds, (first + j * kStep) * kBytes);
     }
   };
-  if (row < a.rows)
-    load_row(row);
+  load_row(row);
   const float cols = (float)a.cols;
-  for (; row < a.rows; row += stride) {
-    // xh and g of this row; columns past the end have dy = w = 0 and add nothing
+  // Teams of several waves meet at barriers: they take the same number of
+  // turns, in the last of which some may have no row.  Such a row, and columns
+  // past the end, read as zeros and add nothing.
+  for (int64_t base = (int64_t)blockIdx.x * kTeams; base < a.rows; base += stride, row += stride) {
+    if (WPR == 1 && row >= a.rows)
+      break;
     float xh[NCH][VEC], g[NCH][VEC];
-    const float mu = mean, rs = rstd;
+    const float mu = rm.get(0), rs = rr.get(0);
     float sg = 0.0f, sx = 0.0f;
 #pragma unroll
     for (int j = 0; j < NCH; ++j) {
-      const bool on = first + j * kStep < a.cols;
 #pragma unroll
       for (int i = 0; i < VEC; ++i) {
         const float d = rd[j].get(i);
-        xh[j][i] = on ? (rx[j].get(i) - mu) * rs : 0.0f;
+        xh[j][i] = (rx[j].get(i) - mu) * rs;
         g[j][i] = d * w[j][i];
         dw[j][i] += d * xh[j][i];
         db[j][i] += d;
@@ -260,33 +280,32 @@ __global__ __launch_bounds__(norm_threads(WPR)) void norm_bwd_kernel(NormArgs a)
         sx += g[j][i] * xh[j][i];
       }
     }
-    if (row + stride < a.rows)
-      load_row(row + stride);
-    const f32x2 s = team_sum<WPR>((f32x2){sg, sx}, slots, turn);
+    // the next row's loads, once this row has left the registers they go to
+    __builtin_amdgcn_sched_barrier(0);
+    load_row(row + stride);
+    const f32x2 s = team_sum<WPR>((f32x2){sg, sx}, slots[team], turn);
     const float mg = s[0] / cols, mx = s[1] / cols;
-    T* dr = dx + row * a.cols;
+    const __amdgpu_buffer_rsrc_t os = row_range<T>(a.out, a.cols, row, a.rows, a.cols);
 #pragma unroll
     for (int j = 0; j < NCH; ++j) {
-      const int c = first + j * kStep;
 #pragma unroll
       for (int i = 0; i < VEC; ++i)
         g[j][i] = rs * (g[j][i] - mg - xh[j][i] * mx);
-      if (c < a.cols)
-        store(dr + c, g[j]);
+      store<T, kDxPolicy>(os, (first + j * kStep) * kBytes, g[j]);
     }
   }
 
   // this workgroup's sums: row 2 b of the workspace for dw, 2 b + 1 for db
   float* pw = a.part + (int64_t)blockIdx.x * 2 * a.cols;
   if constexpr (kTeams > 1) {
-    // four teams share the columns: added up one after the other
+    // the teams share the columns: added up one after the other
     for (int t = 0; t < kTeams; ++t) {
-      if (wave == t) {
+      if (team == t) {
 #pragma unroll
         for (int j = 0; j < NCH; ++j)
 #pragma unroll
           for (int i = 0; i < VEC; ++i) {
-            f32x2& m = meet[(j * VEC + i) * 64 + lane];
+            f32x2& m = meet[((j * VEC + i) * WPR + wave % WPR) * 64 + lane];
             const f32x2 o = t == 0 ? (f32x2){0.0f, 0.0f} : m;
             dw[j][i] += o[0];
             db[j][i] += o[1];
@@ -295,7 +314,7 @@ __global__ __launch_bounds__(norm_threads(WPR)) void norm_bwd_kernel(NormArgs a)
       }
       lds_barrier();
     }
-    if (wave != kTeams - 1)
+    if (team != kTeams - 1)
       return;
   }
 #pragma unroll
@@ -311,25 +330,29 @@ __global__ __launch_bounds__(norm_threads(WPR)) void norm_bwd_kernel(NormArgs a)
   }
 }
 
-// Adds up the workgroups' rows of dw and db sums: 64 columns to a workgroup,
-// its 16 waves take every 16th row, and their sums meet in LDS in order.
-constexpr int kFoldWaves = 16;
+// Adds up the workgroups' rows of dw and db sums: 16 columns to a workgroup,
+// 64 threads to a column, each with every 64th row, so that all loads are in
+// flight at once; then lanes, then waves in LDS, in order.
+constexpr int kFoldCols = 16, kFoldWaves = 16;
 __global__ __launch_bounds__(64 * kFoldWaves) void norm_fold_kernel(const float* part, int32_t rows, int32_t cols,
                                                                     float* dw, float* db) {
-  __shared__ float meet[kFoldWaves][64];
+  __shared__ float meet[kFoldWaves][kFoldCols];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int which = blockIdx.y;   // 0: dw, 1: db
-  const int c = blockIdx.x * 64 + lane;
+  const int c = blockIdx.x * kFoldCols + lane % kFoldCols;
+  constexpr int kStep = 64 * kFoldWaves / kFoldCols;
   float sum = 0.0f;
   if (c < cols) {
     const float* p = part + (int64_t)which * cols + c;
-#pragma unroll 4
-    for (int r = wave; r < rows; r += kFoldWaves)
+#pragma unroll 8
+    for (int r = threadIdx.x / kFoldCols; r < rows; r += kStep)
       sum += p[(int64_t)r * 2 * cols];
   }
-  meet[wave][lane] = sum;
+  sum = across_rows16(sum);
+  if (lane < kFoldCols)
+    meet[wave][lane] = sum;
   lds_barrier();
-  if (wave == 0 && c < cols) {
+  if (wave == 0 && lane < kFoldCols && c < cols) {
 #pragma unroll
     for (int i = 1; i < kFoldWaves; ++i)
       sum += meet[i][lane];
@@ -354,12 +377,11 @@ static NormShape norm_shape(int64_t cols, int vec) {
   return {16, chunks <= 64 * 16 * 4 ? 4 : chunks <= 64 * 16 * 8 ? 8 : 16};
 }
 
-// Workgroups of a launch.  Forward: enough to fill the GPU several times
-// over.  Backward: two to a CU, each with a row of sums to add up afterwards.
-constexpr int64_t kFwdBlocks = 2048;
-constexpr int64_t kBwdBlocks = 512;
-static int64_t norm_blocks(int64_t rows, int wpr, int64_t most) {
-  const int64_t teams = wpr == 1 ? 4 : 1;
+// Workgroups of a forward launch: enough that the last round of them is short
+// (16640 x 8192 bf16 with checkpoint: 2048 133 us, 4096 128 us), few enough
+// that a workgroup loads the weights for several rows.
+constexpr int64_t kFwdBlocks = 4096;
+static int64_t norm_blocks(int64_t rows, int64_t teams, int64_t most) {
   const int64_t want = (rows + teams - 1) / teams;
   return want < most ? want : most;
 }
@@ -370,13 +392,18 @@ template <typename T, int VEC, int WPR, int NCH>
 static hipError_t launch_norm(const NormArgs& a, bool bwd, hipStream_t stream) {
   const dim3 threads(norm_threads(WPR));
   if (bwd) {
-    const int64_t blocks = norm_blocks(a.rows, WPR, kBwdBlocks);
+    const int64_t blocks = norm_blocks(a.rows, norm_bwd_teams(WPR, VEC), norm_bwd_blocks(WPR, VEC));
     if (blocks > 0)
-      hipLaunchKernelGGL((norm_bwd_kernel<T, VEC, WPR, NCH>), dim3((unsigned)blocks), threads, 0, stream, a);
-    hipError_t e = hipGetLastError();
-    return e;
+      hipLaunchKernelGGL((norm_bwd_kernel<T, VEC, WPR, NCH>), dim3((unsigned)blocks),
+                         dim3(64 * WPR * norm_bwd_teams(WPR, VEC)), 0, stream, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess)
+      return e;
+    hipLaunchKernelGGL(norm_fold_kernel, dim3((unsigned)((a.cols + kFoldCols - 1) / kFoldCols), a.db != nullptr ? 2 : 1),
+                       dim3(64 * kFoldWaves), 0, stream, a.part, (int32_t)blocks, a.cols, a.dw, a.db);
+    return hipGetLastError();
   }
-  const dim3 grid((unsigned)norm_blocks(a.rows, WPR, kFwdBlocks));
+  const dim3 grid((unsigned)norm_blocks(a.rows, WPR == 1 ? 4 : 1, kFwdBlocks));
   if constexpr (VEC == 8) {
     if (a.q != nullptr) {
       hipLaunchKernelGGL((norm_fwd_kernel<T, VEC, WPR, NCH, true>), grid, threads, 0, stream, a);
@@ -388,9 +415,8 @@ static hipError_t launch_norm(const NormArgs& a, bool bwd, hipStream_t stream) {
 }
 
 template <typename T, int VEC>
-static hipError_t launch_norm_shape(const NormArgs& a, bool bwd, int* wpr, hipStream_t stream) {
+static hipError_t launch_norm_shape(const NormArgs& a, bool bwd, hipStream_t stream) {
   const NormShape sh = norm_shape(a.cols, VEC);
-  *wpr = sh.wpr;
   if (sh.wpr == 1)
     return sh.nch == 1 ? launch_norm<T, VEC, 1, 1>(a, bwd, stream) : launch_norm<T, VEC, 1, 2>(a, bwd, stream);
   if (sh.wpr == 4) {
@@ -415,11 +441,11 @@ static hipError_t launch_norm_shape(const NormArgs& a, bool bwd, int* wpr, hipSt
     return hipErrorInvalidValue;   // unreachable: 8 x 4 chunks of 8 hold MAX_NORM_COLS
 }
 
-static hipError_t launch_norm_any(const NormArgs& a, bool f32, bool vec, bool bwd, int* wpr, hipStream_t stream) {
+static hipError_t launch_norm_any(const NormArgs& a, bool f32, bool vec, bool bwd, hipStream_t stream) {
   if (f32)
-    return vec ? launch_norm_shape<float, 4>(a, bwd, wpr, stream) : launch_norm_shape<float, 1>(a, bwd, wpr, stream);
-  return vec ? launch_norm_shape<uint16_t, 8>(a, bwd, wpr, stream)
-             : launch_norm_shape<uint16_t, 1>(a, bwd, wpr, stream);
+    return vec ? launch_norm_shape<float, 4>(a, bwd, stream) : launch_norm_shape<float, 1>(a, bwd, stream);
+  return vec ? launch_norm_shape<uint16_t, 8>(a, bwd, stream)
+             : launch_norm_shape<uint16_t, 1>(a, bwd, stream);
 }
 
 hipError_t launch_norm_fwd(const void* x, int64_t ldx, bool x_f32, const void* w, const void* b, bool w_f32,
@@ -428,8 +454,7 @@ hipError_t launch_norm_fwd(const void* x, int64_t ldx, bool x_f32, const void* w
   NormArgs a = {};
   a.x = x, a.ldx = ldx, a.w = w, a.b = b, a.w_f32 = w_f32, a.rows = rows, a.cols = (int32_t)cols, a.eps = eps;
   a.out = y, a.mean = mean, a.rstd = rstd, a.q = q, a.s = s;
-  int wpr;
-  return launch_norm_any(a, x_f32, vec, false, &wpr, stream);
+  return launch_norm_any(a, x_f32, vec, false, stream);
 }
 
 hipError_t launch_norm_bwd(const void* dy, int64_t lddy, const void* x, int64_t ldx, bool x_f32, const void* w,
@@ -438,14 +463,8 @@ hipError_t launch_norm_bwd(const void* dy, int64_t lddy, const void* x, int64_t 
   NormArgs a = {};
   a.x = x, a.ldx = ldx, a.dy = dy, a.lddy = lddy, a.w = w, a.w_f32 = w_f32, a.rows = rows, a.cols = (int32_t)cols;
   a.out = dx, a.mean = const_cast<float*>(mean), a.rstd = const_cast<float*>(rstd), a.part = part;
-  int wpr = 1;
-  const hipError_t e = launch_norm_any(a, x_f32, vec, true, &wpr, stream);
-  if (e != hipSuccess)
-    return e;
-  const int64_t blocks = norm_blocks(rows, wpr, kBwdBlocks);
-  hipLaunchKernelGGL(norm_fold_kernel, dim3((unsigned)((cols + 63) / 64), db != nullptr ? 2 : 1),
-                     dim3(64 * kFoldWaves), 0, stream, part, (int32_t)blocks, (int32_t)cols, dw, db);
-  return hipGetLastError();
+  a.dw = dw, a.db = db;
+  return launch_norm_any(a, x_f32, vec, true, stream);
 }
 
 }  // namespace mx

@@ -320,10 +320,7 @@ __global__ __launch_bounds__(kRouterThreads) void router_fwd_kernel(RouterArgs a
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     if constexpr (G == 16) {
-      const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(psum[v]), __float_as_uint(psum[v]), false, false);
-      psum[v] = __uint_as_float(s[0]) + __uint_as_float(s[1]);
-      const auto t = __builtin_amdgcn_permlane32_swap(__float_as_uint(psum[v]), __float_as_uint(psum[v]), false, false);
-      psum[v] = __uint_as_float(t[0]) + __uint_as_float(t[1]);
+      psum[v] = across_rows16(psum[v]);
     }
   }
   if (rows_here > 0)

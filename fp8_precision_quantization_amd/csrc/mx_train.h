@@ -51,9 +51,13 @@ __device__ __forceinline__ void unpack(const uint16_t* p, float (&f)[N]) {
   }
 }
 
+// Cache policies.  kCacheNT: memory that is not read again soon (a hint).
+// kCacheThrough: stores go through to memory at once.
+constexpr int kCacheNT = 2, kCacheThrough = 17;
+
 // N elements as loaded, one register word per 4 bytes (a bf16 single fills
 // one word): kept raw while in flight, turned into binary32 when used.
-template <typename T, int N>
+template <typename T, int N, int kPolicy = 0>
 struct Raw {
   static constexpr int kWords = N == 1 ? 1 : N * (int)sizeof(T) / 4;
   uint32_t w[kWords];
@@ -74,6 +78,21 @@ struct Raw {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         w[i] = v[i];
+    }
+  }
+  // from a buffer's range, zeros past its end.  (The whole offset is the
+  // lane's: a scalar one is taken off the range's size before the check, which
+  // wraps where it is the larger.)
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t rsrc, int offset) {
+    if constexpr (N * sizeof(T) == 16) {
+      const auto v = __builtin_amdgcn_raw_buffer_load_b128(rsrc, offset, 0, kPolicy);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        w[i] = v[i];
+    } else if constexpr (sizeof(T) == 4) {
+      w[0] = __builtin_amdgcn_raw_buffer_load_b32(rsrc, offset, 0, kPolicy);
+    } else {
+      w[0] = __builtin_amdgcn_raw_buffer_load_b16(rsrc, offset, 0, kPolicy);
     }
   }
   __device__ __forceinline__ float get(int i) const {
@@ -111,6 +130,23 @@ __device__ __forceinline__ void store(T* p, const float (&f)[N]) {
   }
 }
 
+// The same into a buffer's range, dropped past its end; POLICY: the cache
+// policy bits of the store.
+template <typename T, int POLICY, int N>
+__device__ __forceinline__ void store(__amdgpu_buffer_rsrc_t rsrc, int offset, const float (&f)[N]) {
+  if constexpr (N * sizeof(T) == 16 && sizeof(T) == 4)
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, (f32x4){f[0], f[1], f[2], f[3]}), rsrc, offset, 0,
+                                           POLICY);
+  else if constexpr (N * sizeof(T) == 16)
+    __builtin_amdgcn_raw_buffer_store_b128((u32x4){bf16_pair(f[0], f[1]), bf16_pair(f[2], f[3]), bf16_pair(f[4], f[5]),
+                                                   bf16_pair(f[6], f[7])},
+                                           rsrc, offset, 0, POLICY);
+  else if constexpr (sizeof(T) == 4)
+    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(f[0]), rsrc, offset, 0, POLICY);
+  else
+    __builtin_amdgcn_raw_buffer_store_b16((short)bf16_pair(f[0], f[0]), rsrc, offset, 0, POLICY);
+}
+
 // Lane moves inside rows of 16 lanes whose four steps visit every lane:
 // neighbour, neighbouring pair, other half of 8, other half of 16.
 template <int STEP>
@@ -137,6 +173,13 @@ __device__ __forceinline__ uint32_t lanes_reduce(uint32_t v, Op op) {
     static_assert(G == 16, "lanes of a group");
   }
   return v;
+}
+// Sum over the lanes l, l ^ 16, l ^ 32, l ^ 48; every lane gets it.
+__device__ __forceinline__ float across_rows16(float v) {
+  const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+  const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(b[0]) + __uint_as_float(b[1]);
 }
 template <int G = 64>
 __device__ __forceinline__ float lanes_sum(float v) {
