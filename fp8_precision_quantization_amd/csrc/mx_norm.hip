@@ -15,14 +15,20 @@
 // no barrier) or four and more (sums meet in LDS, one barrier each).  A
 // lane holds NCH chunks of VEC elements; chunk c of a row sits in lane c % 64
 // of wave (c / 64) % WPR, so a wave's load covers consecutive memory.  VEC is
-// 16 bytes, or one element where a pointer, the row length or the row pitch
-// is not a multiple of that.  A team walks over rows a grid apart: the weight
+// 16 bytes, or one element in rows shorter than that.  Where a pointer, the
+// row length or the row pitch is not a multiple of 16 bytes (RAGGED), words
+// are moved from and to any element and the row's last word ends at its end:
+// the columns that it shares with the word before are counted once, and
+// written twice with the same value (16640 x 1111 bf16 against single
+// elements: forward 34 -> 25 us, backward 42 -> 33).  A team walks over rows a grid apart: the weight
 // (and in the backward pass the running sums of dw and db) stay in registers
 // over all its rows.
 //
 // The mean is taken off before squaring (two sums, one after the other, both
 // from registers), which keeps the variance exact for rows far from zero; the
 // second sum costs lane moves, not memory.
+#include <algorithm>
+
 #include "mx_train.h"
 #include "mx_train_launch.h"
 #include "mxtrain.h"
@@ -45,9 +51,20 @@ struct NormArgs {
 constexpr int norm_threads(int wpr) { return wpr == 1 ? 256 : 64 * wpr; }
 
 // N weights from column c, of either type (uniform branch, once per kernel).
-template <int N>
+// RAGGED: at any element.
+template <bool RAGGED, int N>
 __device__ __forceinline__ void load_weights(const void* w, bool f32, int c, float (&f)[N]) {
-  if (f32)
+  if constexpr (RAGGED) {
+    if (f32) {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        f[i] = static_cast<const float*>(w)[c + i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        f[i] = bf16_lo(static_cast<const uint16_t*>(w)[c + i]);
+    }
+  } else if (f32)
     unpack(static_cast<const float*>(w) + c, f);
   else
     unpack(static_cast<const uint16_t*>(w) + c, f);
@@ -85,7 +102,7 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t row_range(const void* base, in
   return buffer_rsrc(static_cast<const T*>(base) + (on ? row : 0) * ld, on ? (uint32_t)(cols * (int)sizeof(T)) : 0u);
 }
 
-template <typename T, int VEC, int WPR, int NCH, bool CKPT>
+template <typename T, int VEC, int WPR, int NCH, bool RAGGED, bool CKPT>
 __global__ __launch_bounds__(norm_threads(WPR)) void norm_fwd_kernel(NormArgs a) {
   constexpr int kTeams = WPR == 1 ? 4 : 1;
   __shared__ f32x2 slots[2][WPR];
@@ -95,17 +112,26 @@ __global__ __launch_bounds__(norm_threads(WPR)) void norm_fwd_kernel(NormArgs a)
   const int first = ((WPR == 1 ? 0 : wave) * 64 + lane) * VEC;
   constexpr int kStep = WPR * 64 * VEC, kBytes = sizeof(T);
 
+  // first column of a chunk, and whether one of its columns counts in the sums
+  auto chunk_at = [&](int j) {
+    const int c = first + j * kStep;
+    return RAGGED ? min(c, a.cols - VEC) : c;
+  };
+  auto counts = [&](int j, int i) {
+    const int c = first + j * kStep;
+    return RAGGED ? i >= c - (a.cols - VEC) : c < a.cols;
+  };
+
   float w[NCH][VEC], b[NCH][VEC];
 #pragma unroll
   for (int j = 0; j < NCH; ++j) {
 #pragma unroll
     for (int i = 0; i < VEC; ++i)
       w[j][i] = b[j][i] = 0.0f;
-    const int c = first + j * kStep;
-    if (c < a.cols) {
-      load_weights(a.w, a.w_f32, c, w[j]);
+    if (first + j * kStep < a.cols) {
+      load_weights<RAGGED>(a.w, a.w_f32, chunk_at(j), w[j]);
       if (a.b != nullptr)
-        load_weights(a.b, a.w_f32, c, b[j]);
+        load_weights<RAGGED>(a.b, a.w_f32, chunk_at(j), b[j]);
     }
   }
 
@@ -113,10 +139,17 @@ __global__ __launch_bounds__(norm_threads(WPR)) void norm_fwd_kernel(NormArgs a)
   int64_t row = (int64_t)blockIdx.x * kTeams + (WPR == 1 ? wave : 0);
   Raw<T, VEC> raw[NCH];
   auto load_row = [&](int64_t r) {
-    const __amdgpu_buffer_rsrc_t xs = row_range<T>(a.x, a.ldx, r, a.rows, a.cols);
+    if constexpr (RAGGED) {
+      const T* xr = static_cast<const T*>(a.x) + min(r, a.rows - 1) * a.ldx;
 #pragma unroll
-    for (int j = 0; j < NCH; ++j)
-      raw[j].load(xs, (first + j * kStep) * kBytes);
+      for (int j = 0; j < NCH; ++j)
+        raw[j].load_ragged(xr + chunk_at(j));
+    } else {
+      const __amdgpu_buffer_rsrc_t xs = row_range<T>(a.x, a.ldx, r, a.rows, a.cols);
+#pragma unroll
+      for (int j = 0; j < NCH; ++j)
+        raw[j].load(xs, (first + j * kStep) * kBytes);
+    }
   };
   load_row(row);
   const float cols = (float)a.cols;
@@ -129,7 +162,7 @@ __global__ __launch_bounds__(norm_threads(WPR)) void norm_fwd_kernel(NormArgs a)
 #pragma unroll
       for (int i = 0; i < VEC; ++i) {
         v[j][i] = raw[j].get(i);
-        part += v[j][i];
+        part += !RAGGED || counts(j, i) ? v[j][i] : 0.0f;
       }
       sum += part;
     }
@@ -147,9 +180,9 @@ __global__ __launch_bounds__(norm_threads(WPR)) void norm_fwd_kernel(NormArgs a)
 #pragma unroll
       for (int i = 0; i < VEC; ++i) {
         v[j][i] -= mean;
-        part += v[j][i] * v[j][i];
+        part += !RAGGED || counts(j, i) ? v[j][i] * v[j][i] : 0.0f;
       }
-      sq += first + j * kStep < a.cols ? part : 0.0f;
+      sq += RAGGED || counts(j, 0) ? part : 0.0f;
     }
     const float var = team_sum<WPR>((f32x2){sq, 0.0f}, slots, turn)[0] / cols;
     const float rstd = 1.0f / sqrtf(var + a.eps);
@@ -192,6 +225,9 @@ __global__ __launch_bounds__(norm_threads(WPR)) void norm_fwd_kernel(NormArgs a)
         // one lane of a block; the others' byte goes past the range
         __builtin_amdgcn_raw_buffer_store_b8((char)p.byte, ss, (lane & 3) == 0 ? (first + j * kStep) / MX_BLOCK : 1 << 30,
                                              0, 0);
+      } else if constexpr (RAGGED) {
+        if (first + j * kStep < a.cols)
+          store_ragged(static_cast<T*>(a.out) + row * a.cols + chunk_at(j), v[j]);
       } else {
         store<T, kCacheNT>(ys, (first + j * kStep) * kBytes, v[j]);
       }
@@ -204,17 +240,19 @@ __global__ __launch_bounds__(norm_threads(WPR)) void norm_fwd_kernel(NormArgs a)
 // afterwards, so there are no more than keep the memory busy: one to a CU
 // where a workgroup is eight waves or more, two where it is four.  Two teams
 // of four waves with one workgroup to a CU halve those rows against one team
-// with two (16640 x 5120 bf16 107 -> 97 us); single elements have too few
-// bytes in flight for that (16640 x 1111 bf16: 44 and 62 us).
-constexpr int norm_bwd_teams(int wpr, int vec) { return wpr == 1 ? 4 : wpr == 4 && vec > 1 ? 2 : 1; }
+// with two (16640 x 5120 bf16 107 -> 97 us); more workgroups only add to what
+// is added up (1024: 107 us).  Ragged rows keep one team of
+// four: a team without a row would read one instead of zeros.
+constexpr int norm_bwd_teams(int wpr, bool ragged) { return wpr == 1 ? 4 : wpr == 4 && !ragged ? 2 : 1; }
 constexpr int64_t kBwdBlocks = 512;
-constexpr int64_t norm_bwd_blocks(int wpr, int vec) {
-  return wpr * norm_bwd_teams(wpr, vec) == 4 || vec == 1 ? kBwdBlocks : kBwdBlocks / 2;
+static int64_t norm_bwd_blocks(int64_t rows, int wpr, int teams) {
+  const int64_t most = (wpr * teams == 4 ? kBwdBlocks : kBwdBlocks / 2) * teams;
+  return (std::min(rows, most) + teams - 1) / teams;
 }
 
-template <typename T, int VEC, int WPR, int NCH>
-__global__ __launch_bounds__(64 * WPR * norm_bwd_teams(WPR, VEC)) void norm_bwd_kernel(NormArgs a) {
-  constexpr int kTeams = norm_bwd_teams(WPR, VEC);
+template <typename T, int VEC, int WPR, int NCH, bool RAGGED>
+__global__ __launch_bounds__(64 * WPR * norm_bwd_teams(WPR, RAGGED)) void norm_bwd_kernel(NormArgs a) {
+  constexpr int kTeams = norm_bwd_teams(WPR, RAGGED);
   __shared__ f32x2 slots[kTeams][2][WPR];
   __shared__ f32x2 meet[kTeams == 1 ? 1 : 64 * WPR * NCH * VEC];   // a team's dw and db sums
   int turn = 0;
@@ -224,36 +262,55 @@ __global__ __launch_bounds__(64 * WPR * norm_bwd_teams(WPR, VEC)) void norm_bwd_
   const int first = (wave % WPR * 64 + lane) * VEC;
   constexpr int kStep = WPR * 64 * VEC, kBytes = sizeof(T);
 
+  // first column of a chunk, and whether one of its columns counts in the sums
+  auto chunk_at = [&](int j) {
+    const int c = first + j * kStep;
+    return RAGGED ? min(c, a.cols - VEC) : c;
+  };
+  auto counts = [&](int j, int i) {
+    const int c = first + j * kStep;
+    return RAGGED ? i >= c - (a.cols - VEC) : c < a.cols;
+  };
+
   float w[NCH][VEC], dw[NCH][VEC], db[NCH][VEC];
 #pragma unroll
   for (int j = 0; j < NCH; ++j) {
 #pragma unroll
     for (int i = 0; i < VEC; ++i)
       w[j][i] = dw[j][i] = db[j][i] = 0.0f;
-    const int c = first + j * kStep;
-    if (c < a.cols)
-      load_weights(a.w, a.w_f32, c, w[j]);
+    if (first + j * kStep < a.cols)
+      load_weights<RAGGED>(a.w, a.w_f32, chunk_at(j), w[j]);
   }
 
   const int64_t stride = (int64_t)gridDim.x * kTeams;
   int64_t row = (int64_t)blockIdx.x * kTeams + team;
   // Reads past the caches and stores through them: 16640 x 8192 bf16 161 -> 150
   // us, 16640 x 4096 binary32 153 -> 141 us.  Rows of one wave lose
-  // by it (16640 x 384: 13.9 -> 17.4 us), and so do single elements (16640 x
-  // 1111 bf16: 44 -> 72 us), whose stores need the cache to be joined.
-  constexpr int kInPolicy = VEC > 1 && WPR > 1 ? kCacheNT : 0;
+  // by it (16640 x 384: 13.9 -> 17.4 us), and ragged rows, whose cache lines
+  // two rows share, do without.
+  constexpr int kInPolicy = WPR > 1 ? kCacheNT : 0;
   constexpr int kDxPolicy = kInPolicy == 0 ? kCacheNT : kCacheThrough;
   Raw<T, VEC, kInPolicy> rx[NCH], rd[NCH];
   Raw<float, 1> rm, rr;
   auto load_row = [&](int64_t r) {
-    const __amdgpu_buffer_rsrc_t xs = row_range<T>(a.x, a.ldx, r, a.rows, a.cols);
-    const __amdgpu_buffer_rsrc_t ds = row_range<T>(a.dy, a.lddy, r, a.rows, a.cols);
     rm.load(row_range<float>(a.mean, 1, r, a.rows, 1), 0);
     rr.load(row_range<float>(a.rstd, 1, r, a.rows, 1), 0);
+    if constexpr (RAGGED) {
+      const T* xr = static_cast<const T*>(a.x) + min(r, a.rows - 1) * a.ldx;
+      const T* dr = static_cast<const T*>(a.dy) + min(r, a.rows - 1) * a.lddy;
 #pragma unroll
-    for (int j = 0; j < NCH; ++j) {
-      rx[j].load(xs, (first + j * kStep) * kBytes);
-      rd[j].load(ds, (first + j * kStep) * kBytes);
+      for (int j = 0; j < NCH; ++j) {
+        rx[j].load_ragged(xr + chunk_at(j));
+        rd[j].load_ragged(dr + chunk_at(j));
+      }
+    } else {
+      const __amdgpu_buffer_rsrc_t xs = row_range<T>(a.x, a.ldx, r, a.rows, a.cols);
+      const __amdgpu_buffer_rsrc_t ds = row_range<T>(a.dy, a.lddy, r, a.rows, a.cols);
+#pragma unroll
+      for (int j = 0; j < NCH; ++j) {
+        rx[j].load(xs, (first + j * kStep) * kBytes);
+        rd[j].load(ds, (first + j * kStep) * kBytes);
+      }
     }
   };
   load_row(row);
@@ -276,8 +333,8 @@ __global__ __launch_bounds__(64 * WPR * norm_bwd_teams(WPR, VEC)) void norm_bwd_
         g[j][i] = d * w[j][i];
         dw[j][i] += d * xh[j][i];
         db[j][i] += d;
-        sg += g[j][i];
-        sx += g[j][i] * xh[j][i];
+        sg += !RAGGED || counts(j, i) ? g[j][i] : 0.0f;
+        sx += !RAGGED || counts(j, i) ? g[j][i] * xh[j][i] : 0.0f;
       }
     }
     // the next row's loads, once this row has left the registers they go to
@@ -291,7 +348,12 @@ __global__ __launch_bounds__(64 * WPR * norm_bwd_teams(WPR, VEC)) void norm_bwd_
 #pragma unroll
       for (int i = 0; i < VEC; ++i)
         g[j][i] = rs * (g[j][i] - mg - xh[j][i] * mx);
-      store<T, kDxPolicy>(os, (first + j * kStep) * kBytes, g[j]);
+      if constexpr (RAGGED) {
+        if (first + j * kStep < a.cols)
+          store_ragged(static_cast<T*>(a.out) + row * a.cols + chunk_at(j), g[j]);
+      } else {
+        store<T, kDxPolicy>(os, (first + j * kStep) * kBytes, g[j]);
+      }
     }
   }
 
@@ -319,10 +381,10 @@ __global__ __launch_bounds__(64 * WPR * norm_bwd_teams(WPR, VEC)) void norm_bwd_
   }
 #pragma unroll
   for (int j = 0; j < NCH; ++j) {
-    const int c = first + j * kStep;
-    if (c < a.cols) {
+    const int c = chunk_at(j);
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) {
+    for (int i = 0; i < VEC; ++i) {
+      if (counts(j, i)) {
         pw[c + i] = dw[j][i];
         pw[a.cols + c + i] = db[j][i];
       }
@@ -360,92 +422,106 @@ __global__ __launch_bounds__(64 * kFoldWaves) void norm_fold_kernel(const float*
   }
 }
 
-// Launch shape for a row length: waves to a team and chunks to a lane.
+// Launch shape for a row length: waves to a team and chunks to a lane.  In the
+// backward pass rows of three bf16 chunks stay with one wave: more rows are
+// under way than with teams of four (16640 x 1111 47 -> 33 us).  At four
+// chunks the registers halve that again and nothing is gained (16640 x 2048
+// 43 us either way), nor is it in binary32 (2053 x 1111 14 us).
 struct NormShape {
   int wpr, nch;
 };
-static NormShape norm_shape(int64_t cols, int vec) {
+static NormShape norm_shape(int64_t cols, int vec, bool bwd) {
   const int64_t chunks = (cols + vec - 1) / vec;
   if (chunks <= 64)
     return {1, 1};
   if (chunks <= 64 * 2)
     return {1, 2};
+  if (bwd && vec == 8 && chunks <= 64 * 3)
+    return {1, 3};
   for (int wpr = 4; wpr < 16; wpr *= 2)
     for (int nch = 1; nch <= 4; ++nch)
       if (chunks <= 64 * wpr * nch)
         return {wpr, nch};
-  return {16, chunks <= 64 * 16 * 4 ? 4 : chunks <= 64 * 16 * 8 ? 8 : 16};
+  return {16, 4};
 }
 
 // Workgroups of a forward launch: enough that the last round of them is short
 // (16640 x 8192 bf16 with checkpoint: 2048 133 us, 4096 128 us), few enough
 // that a workgroup loads the weights for several rows.
 constexpr int64_t kFwdBlocks = 4096;
-static int64_t norm_blocks(int64_t rows, int64_t teams, int64_t most) {
-  const int64_t want = (rows + teams - 1) / teams;
-  return want < most ? want : most;
-}
-
 int64_t norm_bwd_part_rows(int64_t rows) { return rows < kBwdBlocks ? rows : kBwdBlocks; }
 
-template <typename T, int VEC, int WPR, int NCH>
-static hipError_t launch_norm(const NormArgs& a, bool bwd, hipStream_t stream) {
-  const dim3 threads(norm_threads(WPR));
-  if (bwd) {
-    const int64_t blocks = norm_blocks(a.rows, norm_bwd_teams(WPR, VEC), norm_bwd_blocks(WPR, VEC));
-    if (blocks > 0)
-      hipLaunchKernelGGL((norm_bwd_kernel<T, VEC, WPR, NCH>), dim3((unsigned)blocks),
-                         dim3(64 * WPR * norm_bwd_teams(WPR, VEC)), 0, stream, a);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess)
-      return e;
-    hipLaunchKernelGGL(norm_fold_kernel, dim3((unsigned)((a.cols + kFoldCols - 1) / kFoldCols), a.db != nullptr ? 2 : 1),
-                       dim3(64 * kFoldWaves), 0, stream, a.part, (int32_t)blocks, a.cols, a.dw, a.db);
-    return hipGetLastError();
-  }
-  const dim3 grid((unsigned)norm_blocks(a.rows, WPR == 1 ? 4 : 1, kFwdBlocks));
-  if constexpr (VEC == 8) {
-    if (a.q != nullptr) {
-      hipLaunchKernelGGL((norm_fwd_kernel<T, VEC, WPR, NCH, true>), grid, threads, 0, stream, a);
-      return hipGetLastError();
-    }
-  }
-  hipLaunchKernelGGL((norm_fwd_kernel<T, VEC, WPR, NCH, false>), grid, threads, 0, stream, a);
+template <typename T, int VEC, int WPR, int NCH, bool RAGGED>
+static hipError_t launch_norm_bwd_kernel(const NormArgs& a, hipStream_t stream) {
+  constexpr int kTeams = norm_bwd_teams(WPR, RAGGED);
+  const int64_t blocks = norm_bwd_blocks(a.rows, WPR, kTeams);
+  if (blocks > 0)
+    hipLaunchKernelGGL((norm_bwd_kernel<T, VEC, WPR, NCH, RAGGED>), dim3((unsigned)blocks), dim3(64 * WPR * kTeams), 0,
+                       stream, a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess)
+    return e;
+  hipLaunchKernelGGL(norm_fold_kernel, dim3((unsigned)((a.cols + kFoldCols - 1) / kFoldCols), a.db != nullptr ? 2 : 1),
+                     dim3(64 * kFoldWaves), 0, stream, a.part, (int32_t)blocks, a.cols, a.dw, a.db);
   return hipGetLastError();
 }
 
-template <typename T, int VEC>
-static hipError_t launch_norm_shape(const NormArgs& a, bool bwd, hipStream_t stream) {
-  const NormShape sh = norm_shape(a.cols, VEC);
-  if (sh.wpr == 1)
-    return sh.nch == 1 ? launch_norm<T, VEC, 1, 1>(a, bwd, stream) : launch_norm<T, VEC, 1, 2>(a, bwd, stream);
-  if (sh.wpr == 4) {
-    switch (sh.nch) {
-      case 1: return launch_norm<T, VEC, 4, 1>(a, bwd, stream);
-      case 2: return launch_norm<T, VEC, 4, 2>(a, bwd, stream);
-      case 3: return launch_norm<T, VEC, 4, 3>(a, bwd, stream);
-      default: return launch_norm<T, VEC, 4, 4>(a, bwd, stream);
+template <typename T, int VEC, int WPR, int NCH, bool RAGGED>
+static hipError_t launch_norm(const NormArgs& a, bool bwd, hipStream_t stream) {
+  if (bwd)
+    return launch_norm_bwd_kernel<T, VEC, WPR, NCH, RAGGED>(a, stream);
+  const dim3 threads(norm_threads(WPR));
+  constexpr int kTeams = WPR == 1 ? 4 : 1;
+  const dim3 grid((unsigned)std::min<int64_t>((a.rows + kTeams - 1) / kTeams, kFwdBlocks));
+  if constexpr (VEC == 8 && !RAGGED) {
+    if (a.q != nullptr) {
+      hipLaunchKernelGGL((norm_fwd_kernel<T, VEC, WPR, NCH, false, true>), grid, threads, 0, stream, a);
+      return hipGetLastError();
     }
   }
-  // longer rows: MAX_NORM_COLS is 8 waves x 4 chunks of 8, 16 x 4 of 4, 16 x
-  // 16 of 1
+  hipLaunchKernelGGL((norm_fwd_kernel<T, VEC, WPR, NCH, RAGGED, false>), grid, threads, 0, stream, a);
+  return hipGetLastError();
+}
+
+template <typename T, int VEC, bool RAGGED>
+static hipError_t launch_norm_shape(const NormArgs& a, bool bwd, hipStream_t stream) {
+  const NormShape sh = norm_shape(a.cols, VEC, bwd);
+  if (sh.wpr == 1) {
+    if (sh.nch <= 2)
+      return sh.nch == 1 ? launch_norm<T, VEC, 1, 1, RAGGED>(a, bwd, stream)
+                         : launch_norm<T, VEC, 1, 2, RAGGED>(a, bwd, stream);
+    if constexpr (VEC == 8)
+      return launch_norm_bwd_kernel<T, VEC, 1, 3, RAGGED>(a, stream);
+  }
+  if (sh.wpr == 4) {
+    switch (sh.nch) {
+      case 1: return launch_norm<T, VEC, 4, 1, RAGGED>(a, bwd, stream);
+      case 2: return launch_norm<T, VEC, 4, 2, RAGGED>(a, bwd, stream);
+      case 3: return launch_norm<T, VEC, 4, 3, RAGGED>(a, bwd, stream);
+      default: return launch_norm<T, VEC, 4, 4, RAGGED>(a, bwd, stream);
+    }
+  }
+  // longer rows: MAX_NORM_COLS is 8 waves x 4 chunks of 8, 16 x 4 of 4
   if (sh.wpr == 8)
-    return sh.nch <= 3 ? launch_norm<T, VEC, 8, 3>(a, bwd, stream) : launch_norm<T, VEC, 8, 4>(a, bwd, stream);
-  if constexpr (VEC == 1)
-    return sh.nch <= 4   ? launch_norm<T, VEC, 16, 4>(a, bwd, stream)
-           : sh.nch <= 8 ? launch_norm<T, VEC, 16, 8>(a, bwd, stream)
-                         : launch_norm<T, VEC, 16, 16>(a, bwd, stream);
-  else if constexpr (VEC == 4)
-    return launch_norm<T, VEC, 16, 4>(a, bwd, stream);
+    return sh.nch <= 3 ? launch_norm<T, VEC, 8, 3, RAGGED>(a, bwd, stream)
+                       : launch_norm<T, VEC, 8, 4, RAGGED>(a, bwd, stream);
+  if constexpr (VEC == 4)
+    return launch_norm<T, VEC, 16, 4, RAGGED>(a, bwd, stream);
   else
-    return hipErrorInvalidValue;   // unreachable: 8 x 4 chunks of 8 hold MAX_NORM_COLS
+    return hipErrorInvalidValue;   // unreachable
+}
+
+template <typename T, int VEC>
+static hipError_t launch_norm_type(const NormArgs& a, bool vec, bool bwd, hipStream_t stream) {
+  if (vec)
+    return launch_norm_shape<T, VEC, false>(a, bwd, stream);
+  if (a.cols >= VEC)
+    return launch_norm_shape<T, VEC, true>(a, bwd, stream);
+  return launch_norm<T, 1, 1, 1, false>(a, bwd, stream);
 }
 
 static hipError_t launch_norm_any(const NormArgs& a, bool f32, bool vec, bool bwd, hipStream_t stream) {
-  if (f32)
-    return vec ? launch_norm_shape<float, 4>(a, bwd, stream) : launch_norm_shape<float, 1>(a, bwd, stream);
-  return vec ? launch_norm_shape<uint16_t, 8>(a, bwd, stream)
-             : launch_norm_shape<uint16_t, 1>(a, bwd, stream);
+  return f32 ? launch_norm_type<float, 4>(a, vec, bwd, stream) : launch_norm_type<uint16_t, 8>(a, vec, bwd, stream);
 }
 
 hipError_t launch_norm_fwd(const void* x, int64_t ldx, bool x_f32, const void* w, const void* b, bool w_f32,

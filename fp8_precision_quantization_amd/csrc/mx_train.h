@@ -80,6 +80,17 @@ struct Raw {
         w[i] = v[i];
     }
   }
+  // 16 bytes at any element
+  __device__ __forceinline__ void load_ragged(const T* p) {
+    static_assert(N * sizeof(T) == 16, "one 16-byte word");
+    struct __attribute__((packed, aligned(sizeof(T)))) Word {
+      u32x4 v;
+    };
+    const u32x4 v = reinterpret_cast<const Word*>(p)->v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      w[i] = v[i];
+  }
   // from a buffer's range, zeros past its end.  (The whole offset is the
   // lane's: a scalar one is taken off the range's size before the check, which
   // wraps where it is the larger.)
@@ -128,6 +139,20 @@ __device__ __forceinline__ void store(T* p, const float (&f)[N]) {
                                                    bf16_pair(f[i + 4], f[i + 5]), bf16_pair(f[i + 6], f[i + 7])};
     }
   }
+}
+
+// The same at any element, 16 bytes.
+template <typename T, int N>
+__device__ __forceinline__ void store_ragged(T* p, const float (&f)[N]) {
+  static_assert(N * sizeof(T) == 16, "one 16-byte word");
+  struct __attribute__((packed, aligned(sizeof(T)))) Word {
+    u32x4 v;
+  };
+  if constexpr (sizeof(T) == 4)
+    reinterpret_cast<Word*>(p)->v = __builtin_bit_cast(u32x4, (f32x4){f[0], f[1], f[2], f[3]});
+  else
+    reinterpret_cast<Word*>(p)->v =
+        (u32x4){bf16_pair(f[0], f[1]), bf16_pair(f[2], f[3]), bf16_pair(f[4], f[5]), bf16_pair(f[6], f[7])};
 }
 
 // The same into a buffer's range, dropped past its end; POLICY: the cache
