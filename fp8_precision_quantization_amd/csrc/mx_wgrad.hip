@@ -778,9 +778,6 @@ static WgradPlan wgrad_plan(int64_t rows, int64_t n, int64_t k, int32_t groups) 
   double cost8, cost4;
   const WgradPlan p8 = wgrad_plan_of<8>(rows, n, k, groups, cost8);
   const WgradPlan p4 = wgrad_plan_of<4>(rows, n, k, groups, cost4);
-#ifdef WG_NB
-  return WG_NB == 8 ? p8 : p4;
-#endif
   return cost8 <= cost4 ? p8 : p4;
 }
 

@@ -1,0 +1,158 @@
+"""The training-step operators captured in a HIP graph, on a stream of the
+caller's, and on rows at every alignment.
+
+Graph: captured once and replayed with eager work and synchronisations
+between; every replay must reproduce the eager outputs byte for byte."""
+import numpy as np
+import pytest
+import torch
+
+import fp8_precision_quantization_amd as mx
+from tests import train_ref as ref
+from tests.gpu_util import device
+
+pytestmark = pytest.mark.gpu
+
+REPLAYS = 4
+
+
+def _work(dev):
+    """(fn, outputs): every operator, with its outputs and workspaces given."""
+    g = torch.Generator().manual_seed(5)
+
+    def normal(*shape, dtype=torch.float32):
+        return torch.randn(*shape, generator=g).to(dev).to(dtype)
+
+    bf, f32, i32, u8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+
+    def empty(*shape, dtype=f32):
+        return torch.empty(*shape, dtype=dtype, device=dev)
+
+    t, c, e, k = 1024, 512, 16, 3
+    x, dy, w, b = normal(t, c, dtype=bf), normal(t, c, dtype=bf), normal(c), normal(c)
+    logits, dgates, dloss = normal(t, e), normal(t, k), normal(1)
+    n1 = (empty(t, c, dtype=bf), empty(t), empty(t), empty(t, c, dtype=u8), empty(t, c // 32, dtype=u8))
+    n2 = (empty(t, c, dtype=bf), empty(c), empty(c))
+    r1 = (empty(t, k, dtype=i32), empty(t, k), empty(t), empty(e, dtype=i32), empty(e, dtype=i32), empty(e), empty(1))
+    r2 = empty(t, e)
+    a1 = (empty(t, c // 2, dtype=bf), empty(t, c, dtype=u8), empty(t, c // 32, dtype=u8))
+    a2 = (empty(t, c, dtype=bf), empty(t, c // 2, dtype=bf))
+    # 2 x 2 tiles over 1024 tokens: cut along them, with sums to add up
+    w1, w2 = empty(c, c), empty(e, 2 * c, c)
+    ends = torch.arange(1, e + 1, dtype=i32, device=dev) * (t // e)
+    dh = normal(t, 2 * c, dtype=bf)
+    spaces = [empty(max(int(s), 16), dtype=u8) for s in (
+        mx.mx_layernorm_backward_workspace_bytes(t, c), mx.mx_router_workspace_bytes(t, e),
+        mx.mx_wgrad_checkpoint_workspace_bytes(t, c, c), mx.mx_wgrad_checkpoint_workspace_bytes(t, 2 * c, c, e))]
+
+    def fn():
+        y, mean, rstd, q, s = mx.mx_layernorm(x, w, b, checkpoint=True, out=n1, raw=True)
+        mx.mx_layernorm_backward(dy, x, w, mean, rstd, out=n2, workspace=spaces[0])
+        chosen, gates, lse, _, _, balance, _ = mx.mx_router_balance(logits, k, normalize=True, align=32, out=r1,
+                                                                    workspace=spaces[1])
+        mx.mx_router_balance_backward(logits, lse, chosen, gates, balance, dgates, dloss, normalize=True, out=r2)
+        _, qh, sh = mx.mx_gated_act(y, "gelu", out=a1, raw=True)
+        mx.mx_gated_act_backward(a1[0], qh, sh, "gelu", recompute=True, out=a2)
+        mx.mx_wgrad_checkpoint(dy, q, s, out=w1, workspace=spaces[2])
+        mx.mx_wgrad_checkpoint(dh, q, s, ends, out=w2, workspace=spaces[3])
+
+    return fn, list(n1) + list(n2) + list(r1) + [r2] + list(a1) + list(a2) + [w1, w2]
+
+
+def _fill(outs):
+    for o in outs:
+        o.view(torch.uint8).fill_(0x5A)
+
+
+def _same(outs, want, what):
+    for i, (o, r) in enumerate(zip(outs, want)):
+        assert torch.equal(o.view(torch.uint8), r), (what, i)
+
+
+def test_graph_replays():
+    dev = device()
+    fn, outs = _work(dev)
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        fn()
+    side.synchronize()
+    want = [o.view(torch.uint8).clone() for o in outs]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        fn()
+    for i in range(REPLAYS):
+        _fill(outs)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        _same(outs, want, "replay %d" % i)
+        _fill(outs)
+        fn()
+        torch.cuda.synchronize()
+        _same(outs, want, "eager after replay %d" % i)
+
+
+def test_on_the_callers_stream():
+    """The work waits for what its own stream holds before it: inputs that a
+    long queue on that stream writes last are the ones it reads."""
+    dev = device()
+    x = torch.zeros(2048, 512, dtype=torch.bfloat16, device=dev)
+    final = torch.randn(2048, 512, generator=torch.Generator().manual_seed(1)).to(dev).bfloat16()
+    w = torch.ones(512, device=dev)
+    want = mx.mx_layernorm(final, w, checkpoint=True, raw=True)
+    want_dw = mx.mx_wgrad_checkpoint(final, want[3], want[4])
+    big = torch.randn(4096, 4096, device=dev)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        for _ in range(4):
+            big = (big @ big).clamp(-1, 1)
+        x.copy_(final)
+        got = mx.mx_layernorm(x, w, checkpoint=True, raw=True)
+        got_dw = mx.mx_wgrad_checkpoint(x, got[3], got[4])
+    side.synchronize()
+    for a, r in zip(got, want):
+        assert torch.equal(a, r)
+    assert torch.equal(got_dw, want_dw)
+
+
+# Columns around a word (4 and 8 elements), a wave of words, several chunks of
+# them, and the longest; a first column at any element of a wider matrix.
+@pytest.mark.parametrize("cols,pad,start", [(3, 2, 1), (4, 1, 1), (5, 0, 0), (7, 2, 1), (8, 1, 0), (9, 3, 2), (64, 5, 3),
+                                            (255, 1, 0), (513, 2, 1), (1023, 0, 0), (1025, 7, 5), (1537, 1, 1),
+                                            (2049, 4, 2), (4103, 1, 0), (8191, 2, 1), (12289, 1, 0), (16383, 1, 1)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_norm_rows_at_any_alignment(cols, pad, start, dtype):
+    """Against binary64.  Tolerances as for the layer norm of whole words: 64 u
+    of the magnitudes that meet (u = 2^-24), and half a bf16 ulp for a bf16
+    result; inputs of order one, far from any cancellation in the mean.  What
+    lies outside the matrix is NaN."""
+    dev, rows = device(), 5
+    tt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    g = torch.Generator().manual_seed(cols)
+
+    def matrix():
+        wide = torch.full((rows, start + cols + pad), float("nan"), dtype=tt, device=dev)
+        view = wide[:, start:start + cols]
+        view.copy_(torch.randn(rows, cols, generator=g).to(tt))
+        return view
+
+    x, dy = matrix(), matrix()
+    w = torch.randn(cols + 1, generator=g).to(dev)[1:]
+    b = torch.randn(cols + 1, generator=g).to(dev)[1:]
+    y, mean, rstd = mx.mx_layernorm(x, w, b)
+    dx, dw, db = mx.mx_layernorm_backward(dy, x, w, mean, rstd)
+    xn, dn, wn, bn = (v.double().cpu().numpy() for v in (x, dy, w, b))
+    want, wm, wr = ref.layernorm(xn, wn, bn, 1e-5)
+    u, half = ref.U32, (ref.half_ulp16 if dtype == "bf16" else lambda a: 0.0)
+    mag = np.abs(xn).mean(1)[:, None]
+    tol = 64 * u * ((np.abs(xn - wm[:, None]) + mag) * wr[:, None] * np.abs(wn) + np.abs(bn))
+    # rstd's relative error, 36 u and the square of the mean's, is within the 64 u above
+    ref.assert_close(y.double().cpu().numpy(), want, tol + half(np.abs(want) + tol), "y")
+    m64, r64 = mean.double().cpu().numpy(), rstd.double().cpu().numpy()
+    wdx, wdw, wdb, xh, gg = ref.layernorm_backward(dn, xn, wn, m64, r64)
+    tol = 64 * u * r64[:, None] * (np.abs(gg) + np.abs(gg).mean(1)[:, None]
+                                   + np.abs(xh) * np.abs(gg * xh).mean(1)[:, None])
+    ref.assert_close(dx.double().cpu().numpy(), wdx, tol + half(np.abs(wdx) + tol), "dx")
+    ref.assert_close(dw.double().cpu().numpy(), wdw, (rows + 64) * u * np.abs(dn * xh).sum(0) + 1e-38, "dweight")
+    ref.assert_close(db.double().cpu().numpy(), wdb, (rows + 64) * u * np.abs(dn).sum(0) + 1e-38, "dbias")
