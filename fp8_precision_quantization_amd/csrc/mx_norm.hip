@@ -7,7 +7,9 @@
 //             mean_row(g xh)); dw = sum_rows dy xh, db = sum_rows dy.
 //
 // Both are bound by memory: forward reads and writes an element once,
-// backward reads two and writes one.  So a row is read once and stays in
+// backward reads two and writes one.  16640 x 5120 bf16: forward 62 us (5.5
+// TB/s), with checkpoint 79 us (5.4), backward 96 us (5.3); 16640 x 8192 94,
+// 122 and 149 us.  So a row is read once and stays in
 // registers between its statistics and its result, and the next row's loads
 // are in flight meanwhile.
 //

@@ -133,7 +133,8 @@ MX_API mx_status mx_router_balance(const void* logits, int64_t ld, int32_t l_typ
  *     gates[i]) / (sum of p over the chosen);
  *   dlogits[e] = p[e] * (dp[e] - sum over i of p[i] * dp[i]),
  * p formed again from the logits and lse.  Rows whose first slot holds -1 get
- * zeros.  chosen entries outside [0, experts) are ignored.
+ * zeros.  chosen entries outside [0, experts) are ignored; a row's others are
+ * distinct, as mx_router_balance leaves them.
  *   dlogits    (rows, experts) of l_type, contiguous.
  */
 MX_API mx_status mx_router_balance_backward(const void* logits, int64_t ld, int32_t l_type, const float* lse,
