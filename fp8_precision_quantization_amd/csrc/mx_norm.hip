@@ -243,9 +243,8 @@ __global__ __launch_bounds__(norm_threads(WPR)) void norm_fwd_kernel(NormArgs a)
 // where a workgroup is eight waves or more, two where it is four.  Two teams
 // of four waves with one workgroup to a CU halve those rows against one team
 // with two (16640 x 5120 bf16 107 -> 97 us); more workgroups only add to what
-// is added up (1024: 107 us).  Ragged rows keep one team of
-// four: a team without a row would read one instead of zeros.
-constexpr int norm_bwd_teams(int wpr, bool ragged) { return wpr == 1 ? 4 : wpr == 4 && !ragged ? 2 : 1; }
+// is added up (1024: 107 us).
+constexpr int norm_bwd_teams(int wpr) { return wpr == 1 ? 4 : wpr == 4 ? 2 : 1; }
 constexpr int64_t kBwdBlocks = 512;
 static int64_t norm_bwd_blocks(int64_t rows, int wpr, int teams) {
   const int64_t most = (wpr * teams == 4 ? kBwdBlocks : kBwdBlocks / 2) * teams;
@@ -253,8 +252,8 @@ static int64_t norm_bwd_blocks(int64_t rows, int wpr, int teams) {
 }
 
 template <typename T, int VEC, int WPR, int NCH, bool RAGGED>
-__global__ __launch_bounds__(64 * WPR * norm_bwd_teams(WPR, RAGGED)) void norm_bwd_kernel(NormArgs a) {
-  constexpr int kTeams = norm_bwd_teams(WPR, RAGGED);
+__global__ __launch_bounds__(64 * WPR * norm_bwd_teams(WPR)) void norm_bwd_kernel(NormArgs a) {
+  constexpr int kTeams = norm_bwd_teams(WPR);
   __shared__ f32x2 slots[kTeams][2][WPR];
   __shared__ f32x2 meet[kTeams == 1 ? 1 : 64 * WPR * NCH * VEC];   // a team's dw and db sums
   int turn = 0;
@@ -326,17 +325,21 @@ __global__ __launch_bounds__(64 * WPR * norm_bwd_teams(WPR, RAGGED)) void norm_b
     float xh[NCH][VEC], g[NCH][VEC];
     const float mu = rm.get(0), rs = rr.get(0);
     float sg = 0.0f, sx = 0.0f;
+    // ragged rows past the end are the last one again: left out
+    const bool on = !RAGGED || WPR == 1 || row < a.rows;
+    if (on) {
 #pragma unroll
-    for (int j = 0; j < NCH; ++j) {
+      for (int j = 0; j < NCH; ++j) {
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) {
-        const float d = rd[j].get(i);
-        xh[j][i] = (rx[j].get(i) - mu) * rs;
-        g[j][i] = d * w[j][i];
-        dw[j][i] += d * xh[j][i];
-        db[j][i] += d;
-        sg += !RAGGED || counts(j, i) ? g[j][i] : 0.0f;
-        sx += !RAGGED || counts(j, i) ? g[j][i] * xh[j][i] : 0.0f;
+        for (int i = 0; i < VEC; ++i) {
+          const float d = rd[j].get(i);
+          xh[j][i] = (rx[j].get(i) - mu) * rs;
+          g[j][i] = d * w[j][i];
+          dw[j][i] += d * xh[j][i];
+          db[j][i] += d;
+          sg += !RAGGED || counts(j, i) ? g[j][i] : 0.0f;
+          sx += !RAGGED || counts(j, i) ? g[j][i] * xh[j][i] : 0.0f;
+        }
       }
     }
     // the next row's loads, once this row has left the registers they go to
@@ -351,7 +354,7 @@ __global__ __launch_bounds__(64 * WPR * norm_bwd_teams(WPR, RAGGED)) void norm_b
       for (int i = 0; i < VEC; ++i)
         g[j][i] = rs * (g[j][i] - mg - xh[j][i] * mx);
       if constexpr (RAGGED) {
-        if (first + j * kStep < a.cols)
+        if (on && first + j * kStep < a.cols)
           store_ragged(static_cast<T*>(a.out) + row * a.cols + chunk_at(j), g[j]);
       } else {
         store<T, kDxPolicy>(os, (first + j * kStep) * kBytes, g[j]);
@@ -455,7 +458,7 @@ int64_t norm_bwd_part_rows(int64_t rows) { return rows < kBwdBlocks ? rows : kBw
 
 template <typename T, int VEC, int WPR, int NCH, bool RAGGED>
 static hipError_t launch_norm_bwd_kernel(const NormArgs& a, hipStream_t stream) {
-  constexpr int kTeams = norm_bwd_teams(WPR, RAGGED);
+  constexpr int kTeams = norm_bwd_teams(WPR);
   const int64_t blocks = norm_bwd_blocks(a.rows, WPR, kTeams);
   if (blocks > 0)
     hipLaunchKernelGGL((norm_bwd_kernel<T, VEC, WPR, NCH, RAGGED>), dim3((unsigned)blocks), dim3(64 * WPR * kTeams), 0,
