@@ -56,6 +56,7 @@
 #include "mx_train_launch.h"
 #include "mxtrain.h"
 
+#include <algorithm>
 #include <type_traits>
 #include <utility>
 
@@ -89,6 +90,7 @@ struct WgTile {
 
 struct WgradArgs {
   const uint16_t* dy;
+  int64_t n_read;          // columns of a row of dy that may be read, n or more
   const uint8_t *q, *s;
   const int32_t* ends;
   void* out;
@@ -318,7 +320,7 @@ __global__ __launch_bounds__(kWgThreads)
   // from kFirstLoad on where dy goes through registers) into slot `slot`.
   // Past the last stage they load zeros.
   const int64_t tokens = hi - lo;
-  Run run_dy = {reinterpret_cast<const uint8_t*>(a.dy + lo * a.lddy + i0), ((tokens - 1) * a.lddy + a.n - i0) * 2,
+  Run run_dy = {reinterpret_cast<const uint8_t*>(a.dy + lo * a.lddy + i0), ((tokens - 1) * a.lddy + a.n_read - i0) * 2,
                 kWgTokens * a.lddy * 2};
   Run run_q = {a.q + lo * a.k + j0, tokens * a.k - j0, kWgTokens * a.k};
   Run run_s = {a.s + lo * ks + j0 / MX_BLOCK, tokens * ks - j0 / MX_BLOCK, kWgTokens * ks};
@@ -712,6 +714,8 @@ struct WgradPlan {
   int32_t piece_stages;
   int64_t blocks, parts;   // workgroups; tiles of pieces' sums
   uint32_t cut;            // one group: tiles that are cut; several: groups that may be
+  double work;             // us of the cost that a workgroup after another spends on stages
+  int64_t copy_cols;       // dy is copied to rows of so many columns if it is not aligned; 0: it is not
 };
 
 // What a plan is weighed with, in us, measured on MI355X: a workgroup's start
@@ -762,6 +766,7 @@ static WgradPlan wgrad_plan_of(int64_t rows, int64_t n, int64_t k, int32_t group
     cost = (double)(tiles / kRound) * (Cost::kStart + Cost::kStage * (double)stages);
     if (cut > 0)
       cost += Cost::kStart + Cost::kStage * (double)((stages + pieces - 1) / pieces);
+    p.work = Cost::kStage * (double)(tiles / kRound * stages + (cut > 0 ? (stages + pieces - 1) / pieces : 0));
     if (pieces > 1)
       cost += kWgFold + Cost::kPart * (double)p.parts;
     return p;
@@ -778,6 +783,7 @@ static WgradPlan wgrad_plan_of(int64_t rows, int64_t n, int64_t k, int32_t group
   // groups of uneven length: the longest of few tiles to a CU sets the time
   const double rounds = (double)(tiles * groups) / (double)kRound;
   const double even = (double)total / (double)groups;
+  p.work = Cost::kStage * even * ((rounds < 1.0 ? 1.0 : rounds) + (rounds < 2.0 ? 1.0 : 0.0));
   cost = (rounds < 1.0 ? 1.0 : rounds) * (Cost::kStart + Cost::kStage * even) + (rounds < 2.0 ? Cost::kStage * even : 0.0);
   return p;
 }
@@ -786,16 +792,49 @@ static WgradPlan wgrad_plan_of(int64_t rows, int64_t n, int64_t k, int32_t group
 // the matrix cores busier (16640 x 4096 x 4096: 380 against 546 us); the
 // smaller ones start and end sooner, two to a CU, and there are four times as
 // many (1024 x 2048 x 2048: 16 against 29 us).
+//
+// Where n is not a multiple of 8, rows of dy are not aligned as a rule, and
+// loads through registers (VEC false) make stages take about 1.55 times as
+// long.  A copy in aligned rows costs a launch (3 us) and its bytes, and is
+// made where that is less.  Without and with it: 16640 x 8191 x 5120 1538 and
+// 1152 us, 16640 x 4095 x 4096 583 and 446, 1024 x 1023 x 1024 24 and 18; 8192 x
+// 257 x 256, where it is not made, 17 and 20.
 static WgradPlan wgrad_plan(int64_t rows, int64_t n, int64_t k, int32_t groups) {
   double cost8, cost4;
   const WgradPlan p8 = wgrad_plan_of<8>(rows, n, k, groups, cost8);
   const WgradPlan p4 = wgrad_plan_of<4>(rows, n, k, groups, cost4);
-  return cost8 <= cost4 ? p8 : p4;
+  WgradPlan p = cost8 <= cost4 ? p8 : p4;
+  const int64_t cols = (n + 7) / 8 * 8;
+  if (n % 8 != 0 && 0.55 * p.work > 3.0 + (double)rows * (double)cols * 4.0 / 4.5e6)
+    p.copy_cols = cols;
+  return p;
 }
+
+static int64_t wgrad_part_bytes(const WgradPlan& p) { return p.parts * (32 * p.nb) * (32 * p.nb) * 4; }
 
 int64_t wgrad_workspace_bytes(int64_t rows, int64_t n, int64_t k, int32_t groups) {
   const WgradPlan p = wgrad_plan(rows, n, k, groups);
-  return p.parts * (32 * p.nb) * (32 * p.nb) * 4;
+  return wgrad_part_bytes(p) + rows * p.copy_cols * 2;
+}
+
+// dy in aligned rows of `cols` columns, zeros past column n: a wave to a row.
+__global__ __launch_bounds__(256) void wgrad_copy_kernel(const uint16_t* dy, int64_t lddy, int64_t rows, int64_t n,
+                                                         int64_t cols, uint16_t* out) {
+  const int lane = threadIdx.x & 63;
+  for (int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); row < rows; row += (int64_t)gridDim.x * 4) {
+    const uint16_t* from = dy + row * lddy;
+    for (int64_t c = 8 * lane; c < cols; c += 512) {
+      u32x4 v = {0, 0, 0, 0};
+      if (c + 8 <= n) {
+        v = *reinterpret_cast<const u32x4_any*>(from + c);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 7; ++e)
+          v[e / 2] |= c + e < n ? (uint32_t)from[c + e] << (16 * (e & 1)) : 0u;
+      }
+      *reinterpret_cast<u32x4*>(out + row * cols + c) = v;
+    }
+  }
 }
 
 int64_t wgrad_grid_blocks(int64_t rows, int64_t n, int64_t k, int32_t groups) {
@@ -827,9 +866,20 @@ hipError_t launch_wgrad(const void* dy, int64_t lddy, const uint8_t* q, const ui
                         bool vec, hipStream_t stream) {
   const WgradPlan p = wgrad_plan(rows, n, k, groups);
   WgradArgs a = {};
-  a.dy = static_cast<const uint16_t*>(dy), a.lddy = lddy, a.q = q, a.s = s, a.ends = ends, a.n = n, a.k = k;
+  a.dy = static_cast<const uint16_t*>(dy), a.lddy = lddy, a.n_read = n, a.q = q, a.s = s, a.ends = ends, a.n = n, a.k = k;
   a.out = dw, a.part = workspace, a.rows = (int32_t)rows, a.groups = groups;
   a.tiles_n = p.tiles_n, a.tiles_k = p.tiles_k, a.whole = p.whole, a.pieces = p.pieces, a.piece_stages = p.piece_stages;
+  if (!vec && p.copy_cols > 0 && rows > 0) {
+    uint16_t* copy = reinterpret_cast<uint16_t*>(reinterpret_cast<uint8_t*>(workspace) + wgrad_part_bytes(p));
+    const int64_t blocks = std::min<int64_t>((rows + 3) / 4, 4096);
+    hipLaunchKernelGGL(wgrad_copy_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, a.dy, lddy, rows, n, p.copy_cols,
+                       copy);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess)
+      return e;
+    a.dy = copy, a.lddy = a.n_read = p.copy_cols;
+    vec = true;
+  }
   return p.nb == 8 ? launch_wgrad_any<8>(a, p, vec, bf16, stream) : launch_wgrad_any<4>(a, p, vec, bf16, stream);
 }
 

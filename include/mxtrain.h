@@ -181,7 +181,8 @@ MX_API mx_status mx_gated_act_backward(const void* dy, const uint8_t* q, const u
  * code times its scale is exact in bf16 except where it is below bf16's
  * normal range (scale bytes 0 and 1), where it is rounded to a multiple of
  * 2^-133.  Where the output has too few tiles to fill the GPU the rows are split and
- * the pieces' binary32 sums, kept in the workspace, are added in a fixed
+ * the pieces' binary32 sums, kept in the workspace (as is a copy of dy in
+ * aligned rows where n is not a multiple of 8), are added in a fixed
  * order.
  *   workspace  mx_wgrad_checkpoint_workspace_bytes(rows, n, k, num_groups)
  *              bytes, 16-byte aligned (NULL allowed where that is 0).

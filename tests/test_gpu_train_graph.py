@@ -156,3 +156,36 @@ def test_norm_rows_at_any_alignment(cols, pad, start, dtype):
     ref.assert_close(dx.double().cpu().numpy(), wdx, tol + half(np.abs(wdx) + tol), "dx")
     ref.assert_close(dw.double().cpu().numpy(), wdw, (rows + 64) * u * np.abs(dn * xh).sum(0) + 1e-38, "dweight")
     ref.assert_close(db.double().cpu().numpy(), wdb, (rows + 64) * u * np.abs(dn).sum(0) + 1e-38, "dbias")
+
+
+@pytest.mark.parametrize("rows,n,k,groups", [(4099, 250, 1056, 1), (1024, 1023, 1024, 1), (700, 9, 8192, 1),
+                                             (2000, 777, 2048, 3), (1, 1001, 8192, 1), (130, 2047, 2048, 2)])
+def test_wgrad_of_unaligned_rows(rows, n, k, groups):
+    """Odd row lengths, long enough that dy may be copied to aligned rows
+    first: a workspace full of NaN, dy between NaN, and the same result as
+    from aligned rows with zeros behind them.  Both are sums of the same
+    products, maybe cut differently: within (2 rows + 64) u of the sum of
+    magnitudes of binary64's (u = 2^-24)."""
+    dev = device()
+    g = torch.Generator().manual_seed(n)
+    wide = torch.full((rows, n + 3), float("nan"), dtype=torch.bfloat16, device=dev)
+    dy = wide[:, 1:n + 1]
+    dy.copy_(torch.randn(rows, n, generator=g).bfloat16())
+    x = torch.randn((rows + 31) // 32 * 32, k, generator=g).to(dev).bfloat16()   # the cast takes whole blocks of rows
+    q, s = (t[:rows] for t in mx.mx_cast_dim0_dim1(x, dim1=False, raw=True)[:2])
+    ends = None
+    if groups > 1:
+        ends = torch.arange(1, groups + 1, dtype=torch.int32, device=dev) * (rows // groups)
+        ends[-1] = rows
+    nbytes = mx.mx_wgrad_checkpoint_workspace_bytes(rows, n, k, groups)
+    space = torch.full((max(nbytes, 16),), 0xFF, dtype=torch.uint8, device=dev)
+    got = mx.mx_wgrad_checkpoint(dy, q, s, ends, workspace=space)
+    value = q.view(torch.float8_e4m3fn).double().reshape(rows, k // 32, 32)
+    value = (value * torch.exp2(s.double() - 127)[:, :, None]).reshape(rows, k)
+    lo = 0
+    for i, hi in enumerate([rows] if ends is None else ends.tolist()):
+        a, b = dy[lo:hi].double(), value[lo:hi]
+        want, mag = a.T.contiguous() @ b, a.abs().T.contiguous() @ b.abs()
+        ref.assert_close((got if ends is None else got[i]).double().cpu().numpy(), want.cpu().numpy(),
+                         ((2 * rows + 64) * ref.U32 * mag).cpu().numpy(), "dw")
+        lo = hi
