@@ -9,6 +9,7 @@ namespace {
 
 constexpr int64_t kMaxGridBlocks = (int64_t)UINT32_MAX / 256;   // work-items of a launch are a 32-bit field
 constexpr int64_t kMaxLd = (int64_t)1 << 31;
+constexpr int64_t kMaxActCols = UINT32_MAX;   // column numbers of the gated activation are 32 bits
 // A stage of the weight gradient addresses 64 rows with 32-bit offsets.
 constexpr int64_t kMaxWgradLd = (int64_t)1 << 22;
 
@@ -40,7 +41,7 @@ mx_status check_router(int64_t ld, int32_t l_type, int64_t rows, int32_t experts
 }
 
 mx_status check_act(int64_t rows, int64_t cols, int32_t act) {
-  if (rows < 0 || cols < 0 || cols % MX_BLOCK != 0 || (act != MX_ACT_SILU && act != MX_ACT_GELU))
+  if (rows < 0 || cols < 0 || cols > kMaxActCols || cols % MX_BLOCK != 0 || (act != MX_ACT_SILU && act != MX_ACT_GELU))
     return MX_ERR_SHAPE;
   if (rows > 0 && cols > ((int64_t)1 << 34) / rows)
     return MX_ERR_SHAPE;

@@ -151,8 +151,8 @@ MX_API mx_status mx_router_balance_backward(const void* logits, int64_t ld, int3
  *         2 * cols / 32), the bytes mx_cast_dim0_dim1 writes for h; or both
  *         NULL (no checkpoint).
  *   act   MX_ACT_SILU or MX_ACT_GELU.
- * rows >= 0, cols >= 0 a multiple of 32, rows * cols <= 2^34, else
- * MX_ERR_SHAPE; h and y 16-byte, q 8-byte aligned, else MX_ERR_ALIGN.
+ * rows >= 0, cols >= 0 a multiple of 32, cols < 2^32, rows * cols <= 2^34,
+ * else MX_ERR_SHAPE; h and y 16-byte, q 8-byte aligned, else MX_ERR_ALIGN.
  */
 MX_API mx_status mx_gated_act(const void* h, int64_t rows, int64_t cols, int32_t act, void* y, uint8_t* q,
                               uint8_t* s, hipStream_t stream);
