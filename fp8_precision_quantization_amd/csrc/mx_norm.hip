@@ -251,6 +251,10 @@ static int64_t norm_bwd_blocks(int64_t rows, int wpr, int teams) {
   return (std::min(rows, most) + teams - 1) / teams;
 }
 
+// Chunks of a lane that every row of a launch shape fills (norm_shape): all but
+// the last, and of 16 waves, which rows of more than 8 x 4 chunks have, two.
+constexpr int norm_full_chunks(int wpr, int nch) { return wpr < 16 ? nch - 1 : 2; }
+
 template <typename T, int VEC, int WPR, int NCH, bool RAGGED>
 __global__ __launch_bounds__(64 * WPR * norm_bwd_teams(WPR)) void norm_bwd_kernel(NormArgs a) {
   constexpr int kTeams = norm_bwd_teams(WPR);
@@ -338,7 +342,11 @@ __global__ __launch_bounds__(64 * WPR * norm_bwd_teams(WPR)) void norm_bwd_kerne
           dw[j][i] += d * xh[j][i];
           db[j][i] += d;
           sg += !RAGGED || counts(j, i) ? g[j][i] : 0.0f;
-          sx += !RAGGED || counts(j, i) ? g[j][i] * xh[j][i] : 0.0f;
+          // (past the end xh = -mu rs, which may overflow where no column of the row does)
+          if constexpr (RAGGED)
+            sx += counts(j, i) ? g[j][i] * xh[j][i] : 0.0f;
+          else
+            sx = j < norm_full_chunks(WPR, NCH) || counts(j, i) ? sx + g[j][i] * xh[j][i] : sx;
         }
       }
     }

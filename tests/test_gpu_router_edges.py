@@ -1,0 +1,51 @@
+"""The router's gradient where the log-sum-exp is large: masks of the type's
+lowest value, and logits with a large offset.
+
+Tolerance as for the router's other tests (u = 2^-24): a gradient is within
+(128 + 8 |z - lse|) 3 u of the magnitudes that meet in it.  lse is a binary32
+here whose own spacing may be far above 1: z - lse is then off by at most the
+logarithm of the number of experts, below 8, from what it would be, which
+enters the exponential's argument (64 u more)."""
+import numpy as np
+import pytest
+import torch
+
+import fp8_precision_quantization_amd as mx
+from tests import train_ref as ref
+from tests.gpu_util import device
+
+pytestmark = pytest.mark.gpu
+
+U, HALF = ref.U32, ref.half_ulp16
+TORCH = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("experts", [8, 48, 256, 300, 1000])
+@pytest.mark.parametrize("normalize", [False, True])
+def test_gradient_of_rows_with_a_large_offset(dtype, experts, normalize):
+    """Rows at the lowest number of their type throughout (everything masked by
+    it), rows of which a part is, rows around +-1e6, +-3000, 40, and 0."""
+    dev = device()
+    rng = np.random.default_rng([41, experts, normalize])
+    lowest = -float(torch.finfo(TORCH[dtype]).max)
+    z = 2.0 * rng.standard_normal((24, experts))
+    z[:2] = lowest
+    z[2, : experts // 2] = lowest
+    z[3] = -lowest
+    for r, off in ((4, 1e6), (5, -1e6), (6, 3000.0), (7, -3000.0), (8, 40.0), (9, -40.0), (10, -1e9), (11, -65504.0)):
+        z[r] += off
+    z = ref.bf16_round(z) if dtype == "bf16" else z.astype(np.float32).astype(np.float64)
+    t = torch.from_numpy(z).to(TORCH[dtype]).to(dev)
+    want = ref.router(z, 3, None, normalize, 1)
+    chosen, gates, lse, _, _, balance, _ = mx.mx_router_balance(t, 3, normalize=normalize)
+    assert np.array_equal(chosen.cpu().numpy(), want["chosen"])
+    dgates, dloss = rng.standard_normal((24, 3)).astype(np.float32), np.float32(0.7)
+    dz = mx.mx_router_balance_backward(t, lse, chosen, gates, balance, torch.from_numpy(dgates).to(dev),
+                                       torch.tensor([dloss], device=dev), normalize=normalize)
+    wz, mag = ref.router_backward(z, want["p"], want["chosen"], want["here"], normalize, want["balance"],
+                                  dgates.astype(np.float64), float(dloss))
+    span = np.minimum(z.max(1, keepdims=True) - z, 100.0).max(1, keepdims=True) + 8.0   # e^-100 is below the 1e-37
+    tol = (192 + 8 * span) * U * 3 * mag
+    ref.assert_close(dz.double().cpu().numpy(), wz, tol + (HALF(np.abs(wz) + tol) if dtype == "bf16" else 0.0) + 1e-37,
+                     "dlogits")
