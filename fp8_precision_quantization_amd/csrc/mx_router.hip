@@ -487,9 +487,26 @@ __global__ __launch_bounds__(kRouterBwdThreads) void router_bwd_kernel(RouterArg
 #pragma unroll
     for (int v = 0; v < V; ++v)
       p[v] = part ? exp_fast(z[v] - lse) : 0.0f;
+    // p is e^(z - lse) over its sum, which is 1 but for lse's rounding: up to
+    // |lse| = 16 that changes p by 2^-21, as the exponential's own error does,
+    // and is left.  A far larger lse (of a row that a mask of the type's lowest
+    // value covers, say) may have lost all of the sum's logarithm.
+    float scale = 1.0f;
+    const bool coarse = part && __builtin_fabsf(lse) > 16.0f;
+    if (__any(coarse)) {
+      float psum = 0.0f;
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        psum += p[v];
+      psum = lanes_sum<G>(psum);
+      scale = coarse ? 1.0f / psum : 1.0f;
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        p[v] *= scale;
+    }
 #pragma unroll
     for (int i = 0; i < kKeep; ++i) {
-      pc[i] = exp_fast(zc[i] - lse);
+      pc[i] = exp_fast(zc[i] - lse) * scale;
       dg += d[i] * gate[i];
       total += pc[i];
     }

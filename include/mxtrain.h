@@ -132,7 +132,8 @@ MX_API mx_status mx_router_balance(const void* logits, int64_t ld, int32_t l_typ
  *     d_j = dgates[j], or with normalize (dgates[j] - sum_i dgates[i] *
  *     gates[i]) / (sum of p over the chosen);
  *   dlogits[e] = p[e] * (dp[e] - sum over i of p[i] * dp[i]),
- * p formed again from the logits and lse.  Rows whose first slot holds -1 get
+ * p formed again from the logits and lse, and scaled to a sum of 1 where lse is
+ * so large that its rounding shows.  Rows whose first slot holds -1 get
  * zeros.  chosen entries outside [0, experts) are ignored; a row's others are
  * distinct, as mx_router_balance leaves them.
  *   dlogits    (rows, experts) of l_type, contiguous.
