@@ -37,6 +37,7 @@ from ._train import (  # noqa: F401
     mx_layernorm,
     mx_layernorm_backward,
     mx_layernorm_backward_workspace_bytes,
+    mx_layernorm_checkpoint,
     mx_router_balance,
     mx_router_balance_backward,
     mx_router_workspace_bytes,

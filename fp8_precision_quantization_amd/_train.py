@@ -155,17 +155,24 @@ def mx_layernorm(x, weight, bias=None, eps: float = 1e-5, checkpoint: bool = Fal
     y = _new(o[0], (rows, cols), x.dtype, dev, "y")
     mean = _new(o[1], (rows,), torch.float32, dev, "mean")
     rstd = _new(o[2], (rows,), torch.float32, dev, "rstd")
-    q = s = None
     if checkpoint:
         if x.dtype != torch.bfloat16 or cols % MX_BLOCK:
             raise ValueError("a checkpoint needs a bfloat16 x and a multiple of %d columns" % MX_BLOCK)
         q = _new_bytes(o[3], (rows, cols), dev, "q")
         s = _new_bytes(o[4], (rows, cols // MX_BLOCK), dev, "s")
+        _call("mx_layernorm_checkpoint", dev, x.data_ptr(), ldx, weight.data_ptr(), _p(bias), _TYPES[weight.dtype],
+              rows, cols, eps, y.data_ptr(), mean.data_ptr(), rstd.data_ptr(), q.data_ptr(), s.data_ptr())
+        return (y, mean, rstd) + _fp8(q, s, raw)
     _call("mx_layernorm", dev, x.data_ptr(), ldx, _TYPES[x.dtype], weight.data_ptr(), _p(bias),
-          _TYPES[weight.dtype], rows, cols, eps, y.data_ptr(), mean.data_ptr(), rstd.data_ptr(), _p(q), _p(s))
-    if not checkpoint:
-        return y, mean, rstd
-    return (y, mean, rstd) + _fp8(q, s, raw)
+          _TYPES[weight.dtype], rows, cols, eps, y.data_ptr(), mean.data_ptr(), rstd.data_ptr(), None, None)
+    return y, mean, rstd
+
+
+def mx_layernorm_checkpoint(x, weight, bias=None, eps: float = 1e-5, out=None, raw: bool = False):
+    """mx_layernorm with checkpoint=True: (y, mean, rstd, q, s).  x, weight,
+    bias and a caller's y and s may start at any element, a caller's q at any
+    eight bytes."""
+    return mx_layernorm(x, weight, bias, eps, True, out, raw)
 
 
 def mx_layernorm_backward_workspace_bytes(rows: int, cols: int) -> int:
@@ -354,6 +361,8 @@ def mx_wgrad_checkpoint(dy, q, s, group_end_offsets=None, out_dtype=torch.float3
 _vp, _i64, _i32, _f32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_float
 SIGNATURES = {
     "mx_layernorm": ([_vp, _i64, _i32, _vp, _vp, _i32, _i64, _i64, _f32, _vp, _vp, _vp, _vp, _vp, _vp], ctypes.c_int),
+    "mx_layernorm_checkpoint": ([_vp, _i64, _vp, _vp, _i32, _i64, _i64, _f32, _vp, _vp, _vp, _vp, _vp, _vp],
+                                ctypes.c_int),
     "mx_layernorm_backward_workspace_bytes": ([_i64, _i64], _i64),
     "mx_layernorm_backward": ([_vp, _i64, _vp, _i64, _i32, _vp, _i32, _vp, _vp, _i64, _i64, _vp, _vp, _vp, _vp, _i64,
                                _vp], ctypes.c_int),

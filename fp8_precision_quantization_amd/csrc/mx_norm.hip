@@ -200,7 +200,8 @@ __global__ __launch_bounds__(norm_threads(WPR)) void norm_fwd_kernel(NormArgs a)
         v[j][i] = v[j][i] * rstd * w[j][i] + b[j][i];
       if constexpr (CKPT) {
         // cols is a multiple of 32, so that the four lanes of a block are all
-        // inside the row or all outside it
+        // inside the row or all outside it; a ragged row's chunks then share no
+        // columns, and the checkpoint lies as that of any other
         uint32_t d[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -221,8 +222,13 @@ __global__ __launch_bounds__(norm_threads(WPR)) void norm_fwd_kernel(NormArgs a)
         }
         const __amdgpu_buffer_rsrc_t qs = buffer_rsrc(a.q + row * a.cols, (uint32_t)a.cols);
         const __amdgpu_buffer_rsrc_t ss = buffer_rsrc(a.s + row * (a.cols / MX_BLOCK), (uint32_t)(a.cols / MX_BLOCK));
-        __builtin_amdgcn_raw_buffer_store_b128((u32x4){d[0], d[1], d[2], d[3]}, ys, (first + j * kStep) * kBytes, 0,
-                                               kCacheNT);
+        if constexpr (RAGGED) {
+          if (first + j * kStep < a.cols)
+            store_ragged(static_cast<T*>(a.out) + row * a.cols + chunk_at(j), v[j]);
+        } else {
+          __builtin_amdgcn_raw_buffer_store_b128((u32x4){d[0], d[1], d[2], d[3]}, ys, (first + j * kStep) * kBytes, 0,
+                                                 kCacheNT);
+        }
         __builtin_amdgcn_raw_buffer_store_b64(c, qs, first + j * kStep, 0, kCacheNT);
         // one lane of a block; the others' byte goes past the range
         __builtin_amdgcn_raw_buffer_store_b8((char)p.byte, ss, (lane & 3) == 0 ? (first + j * kStep) / MX_BLOCK : 1 << 30,
@@ -486,9 +492,9 @@ static hipError_t launch_norm(const NormArgs& a, bool bwd, hipStream_t stream) {
   const dim3 threads(norm_threads(WPR));
   constexpr int kTeams = WPR == 1 ? 4 : 1;
   const dim3 grid((unsigned)std::min<int64_t>((a.rows + kTeams - 1) / kTeams, kFwdBlocks));
-  if constexpr (VEC == 8 && !RAGGED) {
+  if constexpr (VEC == 8) {
     if (a.q != nullptr) {
-      hipLaunchKernelGGL((norm_fwd_kernel<T, VEC, WPR, NCH, false, true>), grid, threads, 0, stream, a);
+      hipLaunchKernelGGL((norm_fwd_kernel<T, VEC, WPR, NCH, RAGGED, true>), grid, threads, 0, stream, a);
       return hipGetLastError();
     }
   }

@@ -53,17 +53,14 @@ bool wgrad_shape_ok(int64_t rows, int64_t n, int64_t k) {
          k % MX_BLOCK == 0;
 }
 
-}  // namespace
-
-extern "C" {
-
-mx_status mx_layernorm(const void* x, int64_t ldx, int32_t x_type, const void* weight, const void* bias,
-                       int32_t w_type, int64_t rows, int64_t cols, float eps, void* y, float* mean, float* rstd,
-                       uint8_t* q, uint8_t* s, hipStream_t stream) {
+// Both forms of the forward pass.  anywhere: a checkpoint may be of rows that
+// are not whole 16-byte words.
+mx_status layernorm(const void* x, int64_t ldx, int32_t x_type, const void* weight, const void* bias, int32_t w_type,
+                    int64_t rows, int64_t cols, float eps, void* y, float* mean, float* rstd, bool ckpt, uint8_t* q,
+                    uint8_t* s, bool anywhere, hipStream_t stream) {
   const mx_status st = check_norm(ldx, x_type, w_type, rows, cols);
   if (st != MX_OK)
     return st;
-  const bool ckpt = q != nullptr || s != nullptr;
   if (ckpt && (x_type != MX_TYPE_BF16 || cols % MX_BLOCK != 0))
     return MX_ERR_SHAPE;
   if (rows == 0 || cols == 0)
@@ -77,10 +74,27 @@ mx_status mx_layernorm(const void* x, int64_t ldx, int32_t x_type, const void* w
     return MX_ERR_ALIGN;
   const bool vec = wide(x, ldx, cols, x_type) && aligned(y, 16) && aligned(weight, 16) &&
                    (bias == nullptr || aligned(bias, 16));
-  if (ckpt && (!vec || !aligned(q, 8)))
+  if (ckpt && ((!vec && !anywhere) || !aligned(q, 8)))
     return MX_ERR_ALIGN;
   return from_hip(mx::launch_norm_fwd(x, ldx, x_type == MX_TYPE_F32, weight, bias, w_type == MX_TYPE_F32, rows, cols,
                                       eps, y, mean, rstd, q, s, vec, stream));
+}
+
+}  // namespace
+
+extern "C" {
+
+mx_status mx_layernorm(const void* x, int64_t ldx, int32_t x_type, const void* weight, const void* bias,
+                       int32_t w_type, int64_t rows, int64_t cols, float eps, void* y, float* mean, float* rstd,
+                       uint8_t* q, uint8_t* s, hipStream_t stream) {
+  return layernorm(x, ldx, x_type, weight, bias, w_type, rows, cols, eps, y, mean, rstd, q != nullptr || s != nullptr,
+                   q, s, false, stream);
+}
+
+mx_status mx_layernorm_checkpoint(const void* x, int64_t ldx, const void* weight, const void* bias, int32_t w_type,
+                                  int64_t rows, int64_t cols, float eps, void* y, float* mean, float* rstd, uint8_t* q,
+                                  uint8_t* s, hipStream_t stream) {
+  return layernorm(x, ldx, MX_TYPE_BF16, weight, bias, w_type, rows, cols, eps, y, mean, rstd, true, q, s, true, stream);
 }
 
 int64_t mx_layernorm_backward_workspace_bytes(int64_t rows, int64_t cols) {

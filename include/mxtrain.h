@@ -58,11 +58,22 @@ extern "C" {
  * MX_ERR_SHAPE (also a bad type, or q on a shape without a checkpoint).
  * Pointers need their element's alignment (MX_ERR_ALIGN); where x, weight,
  * bias and y are 16-byte aligned and cols and ldx are whole 16-byte words,
- * the kernel moves 16 bytes at a time, which q requires (MX_ERR_ALIGN).
+ * the kernel moves whole words, which q requires (MX_ERR_ALIGN):
+ * mx_layernorm_checkpoint is the form without that.
  */
 MX_API mx_status mx_layernorm(const void* x, int64_t ldx, int32_t x_type, const void* weight, const void* bias,
                               int32_t w_type, int64_t rows, int64_t cols, float eps, void* y, float* mean,
                               float* rstd, uint8_t* q, uint8_t* s, hipStream_t stream);
+
+/*
+ * mx_layernorm of a bf16 x with its checkpoint, from rows at any pitch and
+ * start: x, weight, bias and y need their element's alignment only, q 8 bytes'
+ * (MX_ERR_ALIGN).  Rows of whole words take the kernel that mx_layernorm
+ * takes and give the same bits; others are read at any element.
+ */
+MX_API mx_status mx_layernorm_checkpoint(const void* x, int64_t ldx, const void* weight, const void* bias,
+                                         int32_t w_type, int64_t rows, int64_t cols, float eps, void* y, float* mean,
+                                         float* rstd, uint8_t* q, uint8_t* s, hipStream_t stream);
 
 /*
  * Gradients of mx_layernorm, with xh = (x - mean) * rstd and g = dy * weight:

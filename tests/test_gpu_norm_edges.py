@@ -10,7 +10,7 @@ import torch
 
 import fp8_precision_quantization_amd as mx
 from tests import train_ref as ref
-from tests.gpu_util import device
+from tests.gpu_util import assert_bytes_equal, device, host, sentinel
 
 pytestmark = pytest.mark.gpu
 
@@ -49,3 +49,89 @@ def test_gradient_of_a_constant_row_far_out(cols, dtype):
     ref.assert_close(_np(dx), wx, tol + (HALF(np.abs(wx) + tol) if dtype == "bf16" else 0.0) + 1e-38, "dx")
     ref.assert_close(_np(dw), ww, (6 + 64) * U * np.abs(dy * xh).sum(0) + 1e-38, "dweight")
     ref.assert_close(_np(db), wb, (6 + 64) * U * np.abs(dy).sum(0) + 1e-38, "dbias")
+
+
+# columns: one block, lanes left empty, one- and four-wave rows, the longest
+@pytest.mark.parametrize("rows,cols", [(1, 32), (5, 96), (70, 512), (9, 1056), (4, 2080), (3, 5120), (3, 8192), (2, 16384)])
+@pytest.mark.parametrize("pad,start", [(1, 0), (3, 0), (5, 2), (8, 3), (0, 0)])
+@pytest.mark.parametrize("wtype", ["bf16", "f32"])
+def test_checkpoint_of_rows_at_any_alignment(rows, cols, pad, start, wtype, oracle_mod):
+    """x a slice of a wider matrix (NaN around it), weight and bias slices that
+    start at an odd element: y, mean and rstd within the layer norm's
+    tolerances, the checkpoint the cast of y."""
+    dev = device()
+    rng = np.random.default_rng([37, rows, cols, pad, start])
+    x = ref.bf16_round(1.5 * rng.standard_normal((rows, cols)) + 0.3)
+    w = ref.bf16_round(1.0 + 0.3 * rng.standard_normal(cols))
+    b = ref.bf16_round(0.2 * rng.standard_normal(cols))
+    wide = torch.full((rows, start + cols + pad), float("nan"), dtype=torch.bfloat16, device=dev)
+    wide[:, start:start + cols] = _dev(x, "bf16", dev)
+    off = [torch.cat([torch.full((1,), float("nan")), torch.from_numpy(v).float()]).to(TORCH[wtype]).to(dev)[1:]
+           for v in (w, b)]
+    sq, ss = sentinel((rows, cols), dev), sentinel((rows, cols // 32), dev)
+    out = (torch.empty(rows, cols, dtype=torch.bfloat16, device=dev), torch.empty(rows, device=dev),
+           torch.empty(rows, device=dev), sq, ss)
+    y, mean, rstd, q, s = mx.mx_layernorm(wide[:, start:start + cols], off[0], off[1], checkpoint=True, out=out, raw=True)
+    wy, wm, wr = ref.layernorm(x, w, b, 1e-5)
+    mag = np.abs(x).mean(1)
+    ref.assert_close(_np(mean), wm, 64 * U * mag, "mean")
+    ref.assert_close(_np(rstd), wr, wr * (36 * U + (48 * U * mag * wr) ** 2), "rstd")
+    tol = 64 * U * ((np.abs(x - wm[:, None]) + mag[:, None]) * wr[:, None] * np.abs(w) + np.abs(b))
+    tol = tol + np.abs(x - wm[:, None]) * wr[:, None] * np.abs(w) * (48 * U * mag * wr)[:, None] ** 2
+    ref.assert_close(_np(y), wy, tol + HALF(np.abs(wy) + tol), "y")
+    r_q, r_s, _ = ref.checkpoint(oracle_mod, _np(y))
+    assert_bytes_equal(host(q), r_q, "codes")
+    assert_bytes_equal(host(s), r_s, "scales")
+
+
+def test_checkpoint_into_any_element(oracle_mod):
+    """The caller's y and scales may start at any element; the codes need eight
+    bytes' alignment and are refused without."""
+    dev = device()
+    rng = np.random.default_rng(38)
+    x, w = _dev(rng.standard_normal((7, 1056)), "bf16", dev), _dev(rng.standard_normal(1056), "f32", dev)
+    y = torch.zeros(7 * 1056 + 2, dtype=torch.bfloat16, device=dev)
+    s = torch.full((7 * 33 + 2,), 0x5A, dtype=torch.uint8, device=dev)
+    q = torch.full((7 * 1056 + 16,), 0x5A, dtype=torch.uint8, device=dev)
+    stats = torch.empty(7, device=dev), torch.empty(7, device=dev)
+    got = mx.mx_layernorm(x, w, checkpoint=True, raw=True,
+                          out=(y[1:-1].view(7, 1056), *stats, q[8:-8].view(7, 1056), s[1:-1].view(7, 33)))
+    r_q, r_s, _ = ref.checkpoint(oracle_mod, _np(got[0]))
+    assert_bytes_equal(host(got[3]), r_q, "codes")
+    assert_bytes_equal(host(got[4]), r_s, "scales")
+    plain = mx.mx_layernorm(x, w)
+    assert torch.equal(got[1], plain[1]) and torch.equal(got[2], plain[2])
+    assert y[0] == 0 and y[-1] == 0 and s[0] == 0x5A and s[-1] == 0x5A
+    assert (q[:8] == 0x5A).all() and (q[-8:] == 0x5A).all()
+    with pytest.raises(mx.MxError):
+        mx.mx_layernorm(x, w, checkpoint=True, out=(y[1:-1].view(7, 1056), *stats, q[4:-12].view(7, 1056),
+                                                    s[1:-1].view(7, 33)))
+
+
+def test_checkpoint_of_infinities_and_nan_at_any_alignment(oracle_mod):
+    """A weight of Inf or NaN reaches y; the checkpoint is still y's cast, and
+    other rows and blocks keep theirs."""
+    dev = device()
+    rng = np.random.default_rng(39)
+    wide = _dev(rng.standard_normal((4, 131)), "bf16", dev)
+    w = np.ones(128)
+    w[3], w[40], w[70] = np.inf, np.nan, -np.inf
+    y, _, _, q, s = mx.mx_layernorm(wide[:, 1:129], _dev(w, "bf16", dev), checkpoint=True, raw=True)
+    bits = y.view(torch.int16).cpu().numpy().view(np.uint16)
+    r_q, r_s = oracle_mod.cast_dim0(np.concatenate([bits, np.zeros((28, 128), np.uint16)]))
+    assert_bytes_equal(host(q), r_q[:4], "codes")
+    assert_bytes_equal(host(s), r_s[:4], "scales")
+
+
+def test_every_drawn_checkpoint_of_a_slice_runs():
+    """Pitches of 3 and 64 elements more than the row, as a slice of a wider
+    matrix has them, from one row to many; the same bits every time."""
+    dev = device()
+    g = torch.Generator().manual_seed(40)
+    for rows, cols, pad in ((1, 5120, 3), (2, 5120, 3), (333, 64, 3), (257, 2048, 64), (64, 8160, 3), (16640, 1024, 3)):
+        x = torch.randn(rows, cols + pad, generator=g).to(dev).bfloat16()[:, :cols]
+        w = torch.randn(cols, generator=g).to(dev)
+        first = mx.mx_layernorm(x, w, checkpoint=True, raw=True)
+        for _ in range(3):
+            for a, b in zip(first, mx.mx_layernorm(x, w, checkpoint=True, raw=True)):
+                assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))

@@ -31,3 +31,21 @@ def test_gated_act_columns_fit_32_bits(lib):
     longest = (1 << 32) - 32
     assert lib.mx_gated_act(None, 1, longest, 0, P, P, P, None) == NULL
     assert lib.mx_gated_act_backward(None, P, P, 1, longest, 0, P, None, None) == NULL
+
+
+def test_layernorm_checkpoint_validation(lib):
+    """Any pitch and start pass; what the checkpoint itself cannot be does not.
+    (rows 0 returns after the shapes: nothing is launched.)"""
+    def f(x=P, ldx=64, w=P, b=P, wt=1, rows=4, cols=64, y=P, mean=P, rstd=P, q=P, s=P):
+        return lib.mx_layernorm_checkpoint(x, ldx, w, b, wt, rows, cols, 1e-5, y, mean, rstd, q, s, None)
+    odd, half = ctypes.c_void_p(0x10001), ctypes.c_void_p(0x10002)
+    for bad in (dict(wt=2), dict(rows=-1), dict(rows=1 << 31), dict(cols=-32), dict(ldx=63), dict(cols=48),
+                dict(cols=16416, ldx=16416), dict(ldx=(1 << 31) + 1)):
+        assert f(**bad) == SHAPE, bad
+    for bad in (dict(x=None), dict(w=None), dict(y=None), dict(mean=None), dict(rstd=None), dict(q=None), dict(s=None)):
+        assert f(**bad) == NULL, bad
+    for bad in (dict(x=odd), dict(y=odd), dict(w=half), dict(b=half), dict(mean=half), dict(rstd=half),
+                dict(q=ctypes.c_void_p(0x10004))):
+        assert f(**bad) == ALIGN, bad
+        assert f(**{**bad, "ldx": 67}) == ALIGN, bad
+    assert f(rows=0, ldx=67, x=None, y=None, q=None, s=None) == OK
