@@ -143,7 +143,8 @@ def mx_layernorm(x, weight, bias=None, eps: float = 1e-5, checkpoint: bool = Fal
     y as x, mean and rstd float32 (R).  weight (C) and bias (C) or None, bf16
     or float32, both of one type.  With checkpoint=True (bf16, C a multiple of
     32) also the 8-bit checkpoint of y: (y, mean, rstd, q, s), e4m3 / e8m0
-    views, or uint8 if raw.  Rows of x may lie any distance apart."""
+    views, or uint8 if raw.  Rows of x may lie any distance apart.  With C = 0
+    mean and rstd are NaN (0 / 0)."""
     _typed(x, (torch.bfloat16, torch.float32), "x")
     rows, cols, ldx = _matrix(x, "x")
     dev = x.device
@@ -155,6 +156,9 @@ def mx_layernorm(x, weight, bias=None, eps: float = 1e-5, checkpoint: bool = Fal
     y = _new(o[0], (rows, cols), x.dtype, dev, "y")
     mean = _new(o[1], (rows,), torch.float32, dev, "mean")
     rstd = _new(o[2], (rows,), torch.float32, dev, "rstd")
+    if cols == 0:   # the C call writes nothing then
+        mean.fill_(float("nan"))
+        rstd.fill_(float("nan"))
     if checkpoint:
         if x.dtype != torch.bfloat16 or cols % MX_BLOCK:
             raise ValueError("a checkpoint needs a bfloat16 x and a multiple of %d columns" % MX_BLOCK)

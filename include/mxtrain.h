@@ -56,6 +56,8 @@ extern "C" {
  *           and scales (rows, cols / 32).
  * 0 <= rows < 2^31, 0 <= cols <= MX_MAX_NORM_COLS, cols <= ldx <= 2^31, else
  * MX_ERR_SHAPE (also a bad type, or q on a shape without a checkpoint).
+ * With rows or cols 0 nothing is written: mean and rstd of rows without
+ * columns are 0 / 0, and the caller's to set.
  * Pointers need their element's alignment (MX_ERR_ALIGN); where x, weight,
  * bias and y are 16-byte aligned and cols and ldx are whole 16-byte words,
  * the kernel moves whole words, which q requires (MX_ERR_ALIGN):

@@ -135,3 +135,19 @@ def test_every_drawn_checkpoint_of_a_slice_runs():
         for _ in range(3):
             for a, b in zip(first, mx.mx_layernorm(x, w, checkpoint=True, raw=True)):
                 assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+@pytest.mark.parametrize("dtype,checkpoint", [("bf16", False), ("f32", False), ("bf16", True)])
+def test_rows_of_no_columns(dtype, checkpoint):
+    """The mean of nothing is 0 / 0: the statistics are NaN, in a caller's
+    tensors too, and not what memory happened to hold."""
+    dev = device()
+    x, w = torch.empty(5, 0, dtype=TORCH[dtype], device=dev), torch.empty(0, device=dev)
+    given = [x.clone(), torch.full((5,), 7.0, device=dev), torch.full((5,), 7.0, device=dev)]
+    if checkpoint:
+        given += [torch.empty(5, 0, dtype=torch.uint8, device=dev), torch.empty(5, 0, dtype=torch.uint8, device=dev)]
+    for out in (None, given):
+        r = mx.mx_layernorm(x, w, w, checkpoint=checkpoint, out=out, raw=True)
+        assert r[0].shape == (5, 0) and torch.isnan(r[1]).all() and torch.isnan(r[2]).all()
+    dx, dw, db = mx.mx_layernorm_backward(x, x, w, r[1], r[2])
+    assert dx.shape == (5, 0) and dw.shape == (0,) and db.shape == (0,)
