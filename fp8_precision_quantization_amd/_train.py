@@ -102,9 +102,10 @@ def _new_bytes(t, shape, device, name):
 
 
 def _workspace(t, nbytes, device):
-    """(tensor to keep until the call is enqueued, address, bytes)."""
+    """(tensor to keep until the call is enqueued, address, bytes).  A size
+    below 0 is of a shape that the call itself will refuse."""
     if t is None:
-        if nbytes == 0:
+        if nbytes <= 0:
             return None, None, 0
         t = torch.empty(nbytes, dtype=torch.uint8, device=device)
     else:
@@ -355,8 +356,7 @@ def mx_wgrad_checkpoint(dy, q, s, group_end_offsets=None, out_dtype=torch.float3
     if out_dtype not in _TYPES:
         raise ValueError("out_dtype must be float32 or bfloat16")
     dw = _new(out, shape, out_dtype, dev, "out")
-    nbytes = mx_wgrad_checkpoint_workspace_bytes(rows, n, k, groups)
-    ws = _workspace(workspace, max(nbytes, 0), dev)
+    ws = _workspace(workspace, mx_wgrad_checkpoint_workspace_bytes(rows, n, k, groups), dev)
     _call("mx_wgrad_checkpoint", dev, dy.data_ptr(), lddy, q.data_ptr(), s.data_ptr(), rows, n, k,
           _p(group_end_offsets), groups, dw.data_ptr(), _TYPES[out_dtype], ws[1], ws[2])
     return dw

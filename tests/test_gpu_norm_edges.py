@@ -151,3 +151,14 @@ def test_rows_of_no_columns(dtype, checkpoint):
         assert r[0].shape == (5, 0) and torch.isnan(r[1]).all() and torch.isnan(r[2]).all()
     dx, dw, db = mx.mx_layernorm_backward(x, x, w, r[1], r[2])
     assert dx.shape == (5, 0) and dw.shape == (0,) and db.shape == (0,)
+
+
+def test_rows_past_the_longest_are_refused():
+    """The backward pass refuses them as the forward pass does, before it sets
+    up a workspace."""
+    dev = device()
+    x, w, m = torch.zeros(2, 16385, device=dev), torch.ones(16385, device=dev), torch.zeros(2, device=dev)
+    with pytest.raises(mx.MxError):
+        mx.mx_layernorm(x, w)
+    with pytest.raises(mx.MxError):
+        mx.mx_layernorm_backward(x, x, w, m, m)
