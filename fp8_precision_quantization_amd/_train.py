@@ -229,8 +229,8 @@ def mx_router_balance(logits, topk: int, valid=None, normalize: bool = False, al
         raise ValueError("logits must have 1 to %d columns" % MX_MAX_GROUPS)
     if not 1 <= topk <= min(experts, MX_MAX_TOPK):
         raise ValueError("topk must be 1 to %d" % min(experts, MX_MAX_TOPK))
-    if align < 1:
-        raise ValueError("align must be positive")
+    if not 1 <= align <= 0x7FFFFFFF:
+        raise ValueError("align must be positive and fit 32 bits")   # (ctypes would cut it off)
     if valid is not None:
         _vector(valid, (torch.bool, torch.uint8), rows, "valid")
         _same_device(dev, valid=valid)

@@ -49,3 +49,14 @@ def test_gradient_of_rows_with_a_large_offset(dtype, experts, normalize):
     tol = (192 + 8 * span) * U * 3 * mag
     ref.assert_close(dz.double().cpu().numpy(), wz, tol + (HALF(np.abs(wz) + tol) if dtype == "bf16" else 0.0) + 1e-37,
                      "dlogits")
+
+
+def test_align_past_32_bits_is_refused():
+    """An `align` that the C interface's 32 bits cannot hold is an error, not
+    its lower bits."""
+    z = torch.zeros(4, 8, device=device())
+    for align in (1 << 31, 1 << 32, (1 << 32) + 1, (1 << 40) + 32):
+        with pytest.raises(ValueError):
+            mx.mx_router_balance(z, 2, align=align)
+    with pytest.raises(mx.MxError):
+        mx.mx_router_balance(z, 2, align=(1 << 31) - 1)   # fits, but the group ends would not
