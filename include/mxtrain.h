@@ -192,12 +192,12 @@ MX_API mx_status mx_gated_act_backward(const void* dy, const uint8_t* q, const u
  *       no group; an empty group's gradient is zero.
  *   dw  (num_groups, n, k), binary32 or bf16 by dw_type.
  * Products are formed on the bf16 matrix cores and summed in binary32: a
- * code times its scale is exact in bf16 except where it is below bf16's
- * normal range (scale bytes 0 and 1), where it is rounded to a multiple of
- * 2^-133.  Where the output has too few tiles to fill the GPU the rows are split and
- * the pieces' binary32 sums, kept in the workspace (as is a copy of dy in
- * aligned rows where n is not a multiple of 8), are added in a fixed
- * order.
+ * code times its scale is exact in bf16 but for some values under scale bytes
+ * 0, 1 and 2, which reach below bf16's smallest step of 2^-133 and are rounded
+ * to the nearest multiple of it.  Where the output has too few tiles to fill
+ * the GPU the rows are split and the pieces' binary32 sums, kept in the
+ * workspace (as is a copy of dy in aligned rows where n is not a multiple of
+ * 8), are added in a fixed order.
  *   workspace  mx_wgrad_checkpoint_workspace_bytes(rows, n, k, num_groups)
  *              bytes, 16-byte aligned (NULL allowed where that is 0).
  * rows, n >= 0, k >= 0 a multiple of 32, rows < 2^31 - 512, n, k and lddy <=
