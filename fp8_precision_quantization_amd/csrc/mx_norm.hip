@@ -8,10 +8,10 @@
 //
 // Both are bound by memory: forward reads and writes an element once,
 // backward reads two and writes one.  16640 x 5120 bf16: forward 62 us (5.5
-// TB/s), with checkpoint 79 us (5.4), backward 96 us (5.3); 16640 x 8192 94,
-// 122 and 149 us.  So a row is read once and stays in
-// registers between its statistics and its result, and the next row's loads
-// are in flight meanwhile.
+// TB/s), with checkpoint 80 us (5.4), backward 94 us (5.4); binary32: 121 us
+// (5.6) and 172 us (5.9); 16640 x 8192 bf16 94, 122 and 149 us.  So a row is
+// read once and stays in registers between its statistics and its result, and
+// the next row's loads are in flight meanwhile.
 //
 // A row belongs to a team of WPR waves: one wave (four teams to a workgroup,
 // no barrier) or four and more (sums meet in LDS, one barrier each).  A
@@ -22,9 +22,17 @@
 // are moved from and to any element and the row's last word ends at its end:
 // the columns that it shares with the word before are counted once, and
 // written twice with the same value (16640 x 1111 bf16 against single
-// elements: forward 34 -> 25 us, backward 42 -> 33).  A team walks over rows a grid apart: the weight
+// elements: forward 34 -> 25 us, backward 42 -> 33; 22 and 30 now).  Their
+// loads straddle cache lines and go without the buffer range and the streaming
+// policies: with checkpoint 16640 x 5120 at a pitch of 5123 takes 103 us, at
+// 5120 80.  A team walks over rows a grid apart: the weight
 // (and in the backward pass the running sums of dw and db) stay in registers
 // over all its rows.
+//
+// Backward rows of more than 8192 binary32 columns are 16 waves with four
+// chunks a lane: 128 registers each, which is 31 too few (54 in ragged rows);
+// these spill to scratch.  4096 x 16384: 178 us (4.5 TB/s), where 16640 x 5120,
+// which fits, reaches 5.9.
 //
 // The mean is taken off before squaring (two sums, one after the other, both
 // from registers), which keeps the variance exact for rows far from zero; the

@@ -24,9 +24,12 @@
 // the wave chooses again with whole logits, the maximum first and then the
 // lowest column that has it.  65536 rows of 256 bf16 logits, topk 8: 52 us
 // with the second way for all, 26 us with the first (and 8 more to add the
-// workgroups' sums up); the vector instructions of the choices bound it, memory
-// would allow 7 us.  The gradient of 65536 x 256 binary32 logits takes 28 us,
-// 5.0 TB/s.
+// workgroups' sums up).  Vector instructions bound it, where memory would allow
+// 7 us: 710 for a wave's four rows (19 us of issue), 285 of them the keys,
+// maxima and exponentials before the choices, 245 the seven choices after the
+// first, the rest gates, p sums and stores; four waves to a SIMD leave some of
+// the loads' latency uncovered.  Binary32 logits: 32 us (and 8).  The gradient
+// of 65536 x 256 binary32 logits takes 28 us, 5.1 TB/s; of bf16 ones 22 us.
 //
 // Sums over rows (p for the loss) stay in a lane's registers over all its
 // rows, meet in LDS, and leave as one row of partial sums per workgroup; the

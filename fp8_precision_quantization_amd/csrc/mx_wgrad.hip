@@ -22,11 +22,11 @@
 // their share, are cut along the tokens; the pieces' sums are added up in a
 // fixed order by a second kernel.
 //
-// Measured on one MI355X: 16640 x 8192 x 5120, bf16 out, 1060 us (1.32
-// PFLOP/s; the library's bf16 product of that shape 0.91, of its best shape
-// 1.58); the MFMAs take 68% of its cycles, at a clock that they pull down to
-// 2.0 - 2.1 GHz.  16 groups of 16640 tokens, 1024 x 1024,
-// binary32 out, 55 us; 4099 x 250 x 1056 19 us.  These wait for the start and
+// Measured: 16640 x 8192 x 5120, bf16 out, 1030 - 1115 us from one MI355X to
+// another (1.25 - 1.35 PFLOP/s; the library's bf16 product of that shape 0.91,
+// of its best shape 1.58); the MFMAs take 68% of its cycles, at a clock that
+// they pull down to 2.0 - 2.1 GHz.  16 groups of 16640 tokens, 1024 x 1024,
+// binary32 out, 54 - 58 us; 4099 x 250 x 1056 19 us.  These wait for the start and
 // the end of their workgroups (12 us a 256 x 256 tile, 5 us a 128 x 128 one):
 // the first stages' loads, and stores that nothing overlaps.
 //
@@ -798,7 +798,10 @@ static WgradPlan wgrad_plan_of(int64_t rows, int64_t n, int64_t k, int32_t group
 // long.  A copy in aligned rows costs a launch (3 us) and its bytes, and is
 // made where that is less.  Without and with it: 16640 x 8191 x 5120 1538 and
 // 1152 us, 16640 x 4095 x 4096 583 and 446, 1024 x 1023 x 1024 24 and 18; 8192 x
-// 257 x 256, where it is not made, 17 and 20.
+// 257 x 256, where it is not made, 17 and 20.  The workspace is sized by the
+// lengths alone: rows of dy that are unaligned by their pitch or start only, n
+// being a multiple of 8, find no room for a copy and go through registers at
+// any size (16640 x 8192 x 5120 at a pitch of 8195: 1560 us).
 static WgradPlan wgrad_plan(int64_t rows, int64_t n, int64_t k, int32_t groups) {
   double cost8, cost4;
   const WgradPlan p8 = wgrad_plan_of<8>(rows, n, k, groups, cost8);

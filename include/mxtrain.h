@@ -196,8 +196,10 @@ MX_API mx_status mx_gated_act_backward(const void* dy, const uint8_t* q, const u
  * 0, 1 and 2, which reach below bf16's smallest step of 2^-133 and are rounded
  * to the nearest multiple of it.  Where the output has too few tiles to fill
  * the GPU the rows are split and the pieces' binary32 sums, kept in the
- * workspace (as is a copy of dy in aligned rows where n is not a multiple of
- * 8), are added in a fixed order.
+ * workspace, are added in a fixed order.  Where n is not a multiple of 8 and
+ * the product long enough, the workspace also holds a copy of dy in aligned
+ * rows, rows * (n rounded up to 8) * 2 bytes, by far the most of it at large
+ * sizes (16640 x 8191 x 5120: 340 MB, where n = 8192 needs 67 MB).
  *   workspace  mx_wgrad_checkpoint_workspace_bytes(rows, n, k, num_groups)
  *              bytes, 16-byte aligned (NULL allowed where that is 0).
  * rows, n >= 0, k >= 0 a multiple of 32, rows < 2^31 - 512, n, k and lddy <=
