@@ -1,8 +1,9 @@
 """libmxcast: bf16 -> MXFP8 casts, the 128x4 blocked e8m0 scale layout and
-the row-wise and tensor-wise fp8 casts on AMD Instinct MI355X (gfx950), and the training-step
+the row-wise and tensor-wise fp8 casts on AMD Instinct MI355X (gfx950), the training-step
 operators around them (layer norm, MoE router, gated activation and weight gradient from 8-bit
-activation checkpoints), as hand-written HIP kernels behind a C ABI (include/mxcast.h,
-include/mxtrain.h).  This package is the thin Python binding over that ABI;
+activation checkpoints), and the MXFP4 cast with the products and the gated feed-forward block
+that read it, as hand-written HIP kernels behind a C ABI (include/mxcast.h, include/mxtrain.h,
+include/mxfp4.h).  This package is the thin Python binding over that ABI;
 the library is loaded on first use and its absence is an error."""
 from ._binding import (  # noqa: F401
     MX_BLOCK,
@@ -43,4 +44,15 @@ from ._train import (  # noqa: F401
     mx_router_workspace_bytes,
     mx_wgrad_checkpoint,
     mx_wgrad_checkpoint_workspace_bytes,
+)
+from ._fp4 import (  # noqa: F401
+    MX_MAX_DECODE_ROWS,
+    mx_cast_mxfp4,
+    mx_dequantize_mxfp4,
+    mx_gated_ffn,
+    mx_gated_ffn_backward,
+    mx_gated_ffn_decode,
+    mx_gemm_mxfp4,
+    mx_grouped_gemm_mxfp4,
+    mx_linear_decode,
 )

@@ -1,0 +1,297 @@
+// The gated feed-forward block on MX operands: both projections, the
+// activation and the product in one kernel, and its gradient.
+//
+// Forward: g = x Wg^T and u = x Wu^T stand in the same wave's accumulators
+// (mx_mm.h, gated), so that y = act(g) u needs neither in memory:
+// 8 bytes an element of y less than a product and the activation after it.
+// The 8-bit checkpoint of (g, u) that the gradient reads is formed from the
+// accumulators themselves: a block of 32 columns of a row is two lanes'
+// registers.
+//
+// Backward: dy = do Wd, whose tile stays in the accumulators; the checkpoint's
+// codes of the same tile come through LDS; dg = dy u act'(g), du = dy act(g).
+#include "mx_gate.h"
+#include "mx_mm_out.h"
+
+namespace mx {
+
+struct FfnArgs {
+  const uint8_t *q_in, *s_in;   // checkpoint (backward)
+  uint16_t *y, *dh;             // y null: none (backward)
+  uint8_t *q, *s;               // null: no checkpoint
+  bool gelu;
+};
+
+// Everything a block's amax (binary32 magnitude bits) decides, by the MXFP8
+// rule of the casts: kinds 0 finite, 1 with an Inf, 2 with a NaN.
+struct Block8 {
+  uint32_t byte;
+  float limit, scale;   // 448 2^e; 2^e in its exponent field
+  uint32_t kind;
+};
+__device__ __forceinline__ Block8 block8(uint32_t amax) {
+  Block8 b;
+  const uint32_t e = amax >> 23;
+  b.kind = amax < 0x7F800000u ? 0 : amax == 0x7F800000u ? 1 : 2;
+  b.byte = b.kind == 0 ? (e > 8 ? e - 8 : 0) : b.kind == 1 ? 254 : 0xFF;
+  // (in a block with an Inf every finite element is below the limit)
+  b.limit = __uint_as_float(b.kind == 0 ? ((b.byte + 8) << 23) | 0x600000u : 0x7F7FFFFFu);
+  b.scale = __uint_as_float(b.byte << 23);
+  return b;
+}
+__device__ __forceinline__ float clamp8(float f, const Block8& b) {
+  return __builtin_amdgcn_fmed3f(f, -b.limit, b.limit);
+}
+// Four elements -> four e4m3 codes; the convert does not saturate.
+__device__ __forceinline__ uint32_t quant8_f32(float f0, float f1, float f2, float f3, const Block8& b) {
+  i16x2 r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32((i16x2){0, 0}, clamp8(f0, b), clamp8(f1, b), b.scale, false);
+  r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(r, clamp8(f2, b), clamp8(f3, b), b.scale, true);
+  uint32_t c = as_u32(r);
+  if (b.kind != 0) {
+    const float f[4] = {f0, f1, f2, f3};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t bits = __float_as_uint(f[i]);
+      const uint32_t special = b.kind == 2 ? 0x7Fu : (bits & 0x7FFFFFFFu) == 0x7F800000u ? 0x7Eu : 0u;
+      if (special != 0)
+        c = (c & ~(0xFFu << (8 * i))) | ((special | ((bits >> 24) & 0x80u)) << (8 * i));
+    }
+  }
+  return c;
+}
+// Largest magnitude's bits of a lane's 16 and the other half's 16.
+__device__ __forceinline__ uint32_t amax32(const v16f& f) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int v = 0; v < 16; ++v)
+    m = max(m, __float_as_uint(f[v]) & 0x7FFFFFFFu);
+  const auto s = __builtin_amdgcn_permlane32_swap(m, m, false, false);
+  return max(s[0], s[1]);
+}
+
+template <int NB, bool GELU>
+__device__ __forceinline__ void ffn_store(const MmArgs& a, const FfnArgs& o, const MmPlace& p, int64_t col0,
+                                          uint8_t* lds, const v16f (&acc)[NB][NB]) {
+  constexpr int kCols = 16 * NB;   // of this wave
+  using StageY = Staged<kCols * 2>;
+  using StageQ = Staged<kCols>;
+  constexpr int kSize = StageY::kSize + 2 * StageQ::kSize;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 31, h = lane >> 5;
+  uint8_t* mine = lds + wave * kSize;
+  const StageY sy = {mine};
+  const StageQ sq[2] = {{mine + StageY::kSize}, {mine + StageY::kSize + StageQ::kSize}};
+  const int row0 = (wave >> 1) * 32 * NB;
+  const int64_t c0 = col0 + (wave & 1) * kCols;
+  const int n = (int)min((int64_t)kCols, a.n - c0);   // a multiple of 32
+#pragma unroll
+  for (int j = 0; j < NB; ++j) {
+    const int rows = p.rows - row0 - 32 * j;
+    if (rows <= 0 || n <= 0)
+      break;
+    const int64_t first = p.row0 + row0 + 32 * j;
+#pragma unroll
+    for (int i = 0; i < NB / 2; ++i) {
+      const v16f &g = acc[i][j], &u = acc[i + NB / 2][j];
+#pragma unroll
+      for (int v = 0; v < 16; v += 4) {
+        const int col = 32 * i + 2 * v + 4 * h;
+        sy.put(r, col * 2, (u32x2){bf16_pair(act_of<GELU>(g[v]) * u[v], act_of<GELU>(g[v + 1]) * u[v + 1]),
+                                   bf16_pair(act_of<GELU>(g[v + 2]) * u[v + 2], act_of<GELU>(g[v + 3]) * u[v + 3])});
+      }
+      if (o.q != nullptr) {
+        const Block8 bg = block8(amax32(g)), bu = block8(amax32(u));
+#pragma unroll
+        for (int v = 0; v < 16; v += 4) {
+          const int col = 32 * i + 2 * v + 4 * h;
+          sq[0].put(r, col, quant8_f32(g[v], g[v + 1], g[v + 2], g[v + 3], bg));
+          sq[1].put(r, col, quant8_f32(u[v], u[v + 1], u[v + 2], u[v + 3], bu));
+        }
+        // the gate's scale byte by the lower lanes, the factor's by the others
+        if (r < rows && 32 * i < n)
+          o.s[(first + r) * (a.n / 16) + (c0 / 32 + i) + (h ? a.n / 32 : 0)] = (uint8_t)(h ? bu.byte : bg.byte);
+      }
+    }
+    mm_wave_fence();
+    sy.drain(reinterpret_cast<uint8_t*>(o.y + first * a.n + c0), a.n * 2, rows, n * 2);
+    if (o.q != nullptr) {
+      uint8_t* q = o.q + first * 2 * a.n + c0;
+      sq[0].drain(q, 2 * a.n, rows, n);
+      sq[1].drain(q + a.n, 2 * a.n, rows, n);
+    }
+    mm_wave_fence();
+  }
+}
+
+template <int FX, int FW, int NB, bool GROUPED>
+__global__ __launch_bounds__(kMmThreads) __attribute__((amdgpu_waves_per_eu(NB == 4 ? 1 : 2, NB == 4 ? 1 : 2)))
+void ffn_kernel(MmArgs a, FfnArgs o) {
+  using T = MmTile<FX, FW, NB>;
+  __shared__ __attribute__((aligned(256))) uint8_t lds[T::kLds];
+  MmPlace p;
+  if (!mm_place<GROUPED, T::kTile>(a, lds, p))
+    return;
+  const int64_t col0 = (int64_t)p.tn * (T::kTile / 2);
+  v16f acc[NB][NB];
+  mm_tile<FX, FW, NB, true>(a, p, col0, lds, acc);
+  if (o.gelu)
+    ffn_store<NB, true>(a, o, p, col0, lds, acc);
+  else
+    ffn_store<NB, false>(a, o, p, col0, lds, acc);
+}
+
+template <int NB, bool GELU>
+__device__ __forceinline__ void ffn_bwd_store(const MmArgs& a, const FfnArgs& o, const MmPlace& p, int64_t col0,
+                                              uint8_t* lds, const v16f (&acc)[NB][NB]) {
+  constexpr int kCols = 32 * NB;
+  using StageQ = Staged<kCols>;
+  using StageD = Staged<kCols * 2>;
+  constexpr int kSize = 2 * StageQ::kSize + StageD::kSize;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 31, h = lane >> 5;
+  uint8_t* mine = lds + wave * kSize;
+  const StageQ sg = {mine}, su = {mine + StageQ::kSize};
+  const StageD sd = {mine + 2 * StageQ::kSize};
+  const int row0 = (wave >> 1) * 32 * NB;
+  const int64_t c0 = col0 + (wave & 1) * kCols;
+  const int n = (int)min((int64_t)kCols, a.n - c0);   // a multiple of 32
+#pragma unroll
+  for (int j = 0; j < NB; ++j) {
+    const int rows = p.rows - row0 - 32 * j;
+    if (rows <= 0 || n <= 0)
+      break;
+    const int64_t first = p.row0 + row0 + 32 * j;
+    const uint8_t* q = o.q_in + first * 2 * a.n + c0;
+    sg.fill(q, 2 * a.n, rows, n);
+    su.fill(q + a.n, 2 * a.n, rows, n);
+    mm_wave_fence();
+    uint32_t dg[NB][8], du[NB][8], y[NB][8];
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+      uint32_t bg = 0, bu = 0;
+      if (r < rows && 32 * i < n) {
+        const uint8_t* s = o.s_in + (first + r) * (a.n / 16) + (c0 / 32 + i);
+        bg = s[0], bu = s[a.n / 32];
+      }
+      const float vg = scale_of(bg), vu = scale_of(bu);
+#pragma unroll
+      for (int v = 0; v < 16; v += 4) {
+        const int col = 32 * i + 2 * v + 4 * h;
+        const int cg = (int)sg.template get<uint32_t>(r, col), cu = (int)su.template get<uint32_t>(r, col);
+        const f32x2 g0 = __builtin_amdgcn_cvt_pk_f32_fp8(cg, false), g1 = __builtin_amdgcn_cvt_pk_f32_fp8(cg, true);
+        const f32x2 u0 = __builtin_amdgcn_cvt_pk_f32_fp8(cu, false), u1 = __builtin_amdgcn_cvt_pk_f32_fp8(cu, true);
+        const float g[4] = {g0[0] * vg, g0[1] * vg, g1[0] * vg, g1[1] * vg};
+        const float u[4] = {u0[0] * vu, u0[1] * vu, u1[0] * vu, u1[1] * vu};
+        float fg[4], fu[4], fy[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float s, dt;
+          gate<GELU>(g[e], s, dt);
+          const float dy = acc[i][j][v + e], act = g[e] * s;
+          fu[e] = dy * act;
+          fg[e] = dy * u[e] * (s + dt * s * (1.0f - s));
+          fy[e] = act * u[e];
+        }
+        dg[i][v / 2] = bf16_pair(fg[0], fg[1]), dg[i][v / 2 + 1] = bf16_pair(fg[2], fg[3]);
+        du[i][v / 2] = bf16_pair(fu[0], fu[1]), du[i][v / 2 + 1] = bf16_pair(fu[2], fu[3]);
+        y[i][v / 2] = bf16_pair(fy[0], fy[1]), y[i][v / 2 + 1] = bf16_pair(fy[2], fy[3]);
+      }
+    }
+    auto leave = [&](const uint32_t (&w)[NB][8], uint16_t* dst, int64_t ld) {
+#pragma unroll
+      for (int i = 0; i < NB; ++i)
+#pragma unroll
+        for (int v = 0; v < 16; v += 4)
+          sd.put(r, (32 * i + 2 * v + 4 * h) * 2, (u32x2){w[i][v / 2], w[i][v / 2 + 1]});
+      mm_wave_fence();
+      sd.drain(reinterpret_cast<uint8_t*>(dst), ld * 2, rows, n * 2);
+      mm_wave_fence();
+    };
+    uint16_t* dh = o.dh + first * 2 * a.n + c0;
+    leave(dg, dh, 2 * a.n);
+    leave(du, dh + a.n, 2 * a.n);
+    if (o.y != nullptr)
+      leave(y, o.y + first * a.n + c0, a.n);
+  }
+}
+
+template <int FX, int FW, int NB, bool GROUPED>
+__global__ __launch_bounds__(kMmThreads) __attribute__((amdgpu_waves_per_eu(NB == 4 ? 1 : 2, NB == 4 ? 1 : 2)))
+void ffn_bwd_kernel(MmArgs a, FfnArgs o) {
+  using T = MmTile<FX, FW, NB>;
+  __shared__ __attribute__((aligned(256))) uint8_t lds[T::kLds];
+  static_assert(4 * (2 * Staged<32 * NB>::kSize + Staged<64 * NB>::kSize) <= T::kLds, "the epilogue's rows");
+  MmPlace p;
+  if (!mm_place<GROUPED, T::kTile>(a, lds, p))
+    return;
+  const int64_t col0 = (int64_t)p.tn * T::kTile;
+  v16f acc[NB][NB];
+  mm_tile<FX, FW, NB, false>(a, p, col0, lds, acc);
+  if (o.gelu)
+    ffn_bwd_store<NB, true>(a, o, p, col0, lds, acc);
+  else
+    ffn_bwd_store<NB, false>(a, o, p, col0, lds, acc);
+}
+
+static constexpr int32_t E4 = MX_FORMAT_E4M3, E2 = MX_FORMAT_E2M1;
+
+template <int FX, int FW, int NB>
+static void launch_pair(bool bwd, const MmArgs& a, const FfnArgs& o, dim3 grid, hipStream_t stream) {
+  const dim3 threads(kMmThreads);
+  if (bwd) {
+    if (a.ends != nullptr)
+      hipLaunchKernelGGL((ffn_bwd_kernel<FX, FW, NB, true>), grid, threads, 0, stream, a, o);
+    else
+      hipLaunchKernelGGL((ffn_bwd_kernel<FX, FW, NB, false>), grid, threads, 0, stream, a, o);
+  } else {
+    if (a.ends != nullptr)
+      hipLaunchKernelGGL((ffn_kernel<FX, FW, NB, true>), grid, threads, 0, stream, a, o);
+    else
+      hipLaunchKernelGGL((ffn_kernel<FX, FW, NB, false>), grid, threads, 0, stream, a, o);
+  }
+}
+
+static hipError_t launch_either(bool bwd, const MmOperands& in, int64_t m, int64_t n, int64_t k, const FfnArgs& o,
+                                hipStream_t stream) {
+  const int nb = mm_blocks(m, n, in.groups, bwd ? 256 : 128);
+  MmArgs a = mm_args(in, m, n, bwd ? n : 2 * n, k);
+  const dim3 grid((unsigned)mm_grid(a, 64 * nb, bwd ? 64 * nb : 32 * nb));
+  if (in.x_format == E2) {
+    if (nb == 4)
+      launch_pair<E2, E2, 4>(bwd, a, o, grid, stream);
+    else
+      launch_pair<E2, E2, 2>(bwd, a, o, grid, stream);
+  } else if (in.w_format == E2) {
+    if (nb == 4)
+      launch_pair<E4, E2, 4>(bwd, a, o, grid, stream);
+    else
+      launch_pair<E4, E2, 2>(bwd, a, o, grid, stream);
+  } else {
+    if (nb == 4)
+      launch_pair<E4, E4, 4>(bwd, a, o, grid, stream);
+    else
+      launch_pair<E4, E4, 2>(bwd, a, o, grid, stream);
+  }
+  return hipGetLastError();
+}
+
+int64_t ffn_grid_blocks(int64_t m, int64_t n, int32_t groups) {
+  MmArgs a = {};
+  static const int32_t some = 0;
+  a.m = m, a.n = n, a.ends = groups > 0 ? &some : nullptr, a.groups = groups;
+  return mm_grid(a, 128, 64);   // the smaller tiles
+}
+
+hipError_t launch_ffn(const MmOperands& in, int64_t m, int64_t n, int64_t k, bool gelu, void* y, uint8_t* q, uint8_t* s,
+                      hipStream_t stream) {
+  FfnArgs o = {};
+  o.y = static_cast<uint16_t*>(y), o.q = q, o.s = s, o.gelu = gelu;
+  return launch_either(false, in, m, n, k, o, stream);
+}
+
+hipError_t launch_ffn_bwd(const MmOperands& in, int64_t m, int64_t n, int64_t k, bool gelu, const uint8_t* q,
+                          const uint8_t* s, void* dh, void* y, hipStream_t stream) {
+  FfnArgs o = {};
+  o.q_in = q, o.s_in = s, o.dh = static_cast<uint16_t*>(dh), o.y = static_cast<uint16_t*>(y), o.gelu = gelu;
+  return launch_either(true, in, m, n, k, o, stream);
+}
+
+}  // namespace mx

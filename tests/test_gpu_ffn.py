@@ -1,0 +1,213 @@
+"""The gated feed-forward block on MX operands and its gradient on the GPU
+against binary64.
+
+Tolerances: the sums' (tests/fp4_ref.py, product_error), carried through the
+activation, and the output's one rounding.  The checkpoint is a cast of numbers
+that may be off by the sums' error: its scale bytes and values lie between
+those of the ends of that range."""
+import numpy as np
+import pytest
+import torch
+
+import fp8_precision_quantization_amd as mx
+from tests import fp4_ref as r4
+from tests import train_ref as ref
+from tests.gpu_util import device, host, sentinel, to_dev_u8
+
+pytestmark = pytest.mark.gpu
+
+PAIRS = [("e4m3", "e4m3"), ("e4m3", "e2m1"), ("e2m1", "e2m1")]
+NAMES = {"e4m3": "mxfp8", "e2m1": "mxfp4"}
+HALF, U = ref.half_ulp16, ref.U32
+
+
+def _np(t):
+    return t.detach().double().cpu().numpy()
+
+
+def _operands(oracle_mod, rng, dev, rows, n, k, fx, fw, ends):
+    """Device operands, values of X and of each group's W; sums of order 1."""
+    g = 1 if ends is None else len(ends)
+    qx, sx = r4.operand(rng, rows, k, fx)
+    qw, sw = r4.operand(rng, g * n, k, fw)
+    down = np.uint8(round(np.log2(16 * np.sqrt(k) * (8 if fx == fw == "e4m3" else 2))))
+    sw = sw - down
+    x, w = r4.values(qx, sx, fx), r4.values(qw, sw, fw).reshape(g, n, k)
+    if ends is None:
+        return [to_dev_u8(v, dev) for v in (qx, oracle_mod.to_blocked(sx), qw, oracle_mod.to_blocked(sw))], None, x, w
+    off = np.asarray(ends, np.int32)
+    sx_b, _ = oracle_mod.to_blocked_grouped(sx, off, 0)
+    sw_b = np.stack([oracle_mod.to_blocked(s) for s in sw.reshape(g, n, -1)])
+    return ([to_dev_u8(v, dev) for v in (qx, sx_b, qw.reshape(g, n, -1), sw_b)], torch.from_numpy(off).to(dev), x, w)
+
+
+def _check_forward(y, q, s, x, w, fx, fw, act, what):
+    k = x.shape[1]
+    h, mag = r4.product(x, w)
+    eh = r4.product_error(mag, k, fx, fw)
+    want = r4.gated(h, act)
+    ref.assert_close(_np(y), want, r4.round_tol(want, r4.gated_tol(h, eh, act), True), what + " y")
+    if q is not None:
+        lo, hi, held = r4.checkpoint_range(h, eh)
+        got_s = host(s)
+        assert np.all((got_s >= lo) & (got_s <= hi)), what + " scales"
+        v = ref.values(host(q), got_s)
+        a, b = held(got_s)
+        assert np.all((v >= a) & (v <= b)), what + " codes"
+
+
+SIZES = [(1, 32, 32), (3, 32, 64), (33, 96, 160), (128, 64, 128), (130, 160, 288), (257, 128, 1056), (64, 1056, 416)]
+
+
+@pytest.mark.parametrize("rows,f,k", SIZES)
+@pytest.mark.parametrize("fx,fw", PAIRS)
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_forward(rows, f, k, fx, fw, act, oracle_mod):
+    dev = device()
+    rng = np.random.default_rng([rows, f, k, act == "gelu"])
+    args, _, x, w = _operands(oracle_mod, rng, dev, rows, 2 * f, k, fx, fw, None)
+    kw = dict(act=act, a_format=NAMES[fx], w_format=NAMES[fw])
+    out = (torch.full((rows, f), float("nan"), dtype=torch.bfloat16, device=dev), sentinel((rows, 2 * f), dev),
+           sentinel((rows, f // 16), dev))
+    y, q, s = mx.mx_gated_ffn(*args, out=out, raw=True, **kw)
+    _check_forward(y, q, s, x, w[0], fx, fw, act, "dense")
+    only, = mx.mx_gated_ffn(*args, checkpoint=False, **kw)
+    assert torch.equal(only, y)
+
+
+GROUPED = [(1, 32, 32, [1]), (100, 96, 96, [0, 1, 1, 60, 97]), (700, 64, 288, [130, 130, 514, 700]),
+           (90, 32, 64, [40, 10, 200])]
+
+
+@pytest.mark.parametrize("rows,f,k,ends", GROUPED)
+@pytest.mark.parametrize("fx,fw", PAIRS)
+def test_forward_grouped(rows, f, k, ends, fx, fw, oracle_mod):
+    dev = device()
+    rng = np.random.default_rng([rows, f, k])
+    args, off, x, w = _operands(oracle_mod, rng, dev, rows, 2 * f, k, fx, fw, ends)
+    out = (torch.full((rows, f), -77.0, dtype=torch.bfloat16, device=dev), sentinel((rows, 2 * f), dev),
+           sentinel((rows, f // 16), dev))
+    y, q, s = mx.mx_gated_ffn(*args, act="gelu", group_end_offsets=off, a_format=NAMES[fx], w_format=NAMES[fw], out=out,
+                              raw=True)
+    for i, (lo, hi) in enumerate(r4.bounds(ends, rows)):
+        if hi > lo:
+            _check_forward(y[lo:hi], q[lo:hi], s[lo:hi], x[lo:hi], w[i], fx, fw, "gelu", "group %d" % i)
+    assert bool((y[hi:] == -77).all()) and bool((q[hi:] == 0xCD).all()) and bool((s[hi:] == 0xCD).all())
+
+
+def _kept(rng, rows, f):
+    """A checkpoint of (g, u) over the range where the activation bends."""
+    s = rng.integers(112, 124, (rows, f // 16)).astype(np.uint8)
+    q = rng.integers(0, 256, (rows, 2 * f)).astype(np.uint8)
+    q = np.where((q & 127) == 127, q ^ 1, q).astype(np.uint8)
+    return q, s, ref.values(q, s)
+
+
+def _check_backward(dh, y, d, w, h, fx, fw, act, what):
+    f, k = h.shape[1] // 2, d.shape[1]
+    g, u = h[:, :f], h[:, f:]
+    dy, mag = r4.product(d, w)
+    edy = r4.product_error(mag, k, fx, fw)
+    wg, wu = ref.gated_act_backward(dy, g, u, act)
+    t, dt = ref.gate_t(g, act)
+    sg = ref.logistic(t)
+    e = (18 + 8 * np.minimum(np.abs(t), 200.0)) * U
+    size = np.abs(dy) + edy
+    cg, cu = np.abs(u) * (sg + np.minimum(np.abs(g * dt), 1e6) * sg), np.abs(g * sg)
+    got = _np(dh)
+    # the coefficients: |act'| <= sg + |g t'| sg; each off by 2 e of that bound
+    tol = edy * cg + 2 * e * size * cg + 2.0 ** -125 * size * np.abs(u)
+    ref.assert_close(got[:, :f], wg, r4.round_tol(wg, tol, True), what + " dgate")
+    tol = edy * cu + e * size * cu + 2.0 ** -125 * size * np.abs(g)
+    ref.assert_close(got[:, f:], wu, r4.round_tol(wu, tol, True), what + " dfactor")
+    if y is not None:
+        want = ref.gated_act(g, u, act)
+        tol = e * np.abs(want) + 2.0 ** -125 * np.abs(g * u)
+        ref.assert_close(_np(y), want, r4.round_tol(want, tol, True), what + " y")
+
+
+@pytest.mark.parametrize("rows,f,k", SIZES)
+@pytest.mark.parametrize("fx,fw", PAIRS)
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_backward(rows, f, k, fx, fw, act, oracle_mod):
+    dev = device()
+    rng = np.random.default_rng([rows, f, k, 7])
+    args, _, d, w = _operands(oracle_mod, rng, dev, rows, f, k, fx, fw, None)
+    q, s, h = _kept(rng, rows, f)
+    kept = (to_dev_u8(q, dev), to_dev_u8(s, dev))
+    kw = dict(act=act, a_format=NAMES[fx], w_format=NAMES[fw])
+    out = tuple(torch.full((rows, n), float("nan"), dtype=torch.bfloat16, device=dev) for n in (2 * f, f))
+    dh, y = mx.mx_gated_ffn_backward(*args, *kept, recompute=True, out=out, **kw)
+    _check_backward(dh, y, d, w[0], h, fx, fw, act, "dense")
+    only, = mx.mx_gated_ffn_backward(*args, *kept, **kw)
+    assert torch.equal(only, dh)
+
+
+@pytest.mark.parametrize("rows,f,k,ends", GROUPED)
+@pytest.mark.parametrize("fx,fw", PAIRS)
+def test_backward_grouped(rows, f, k, ends, fx, fw, oracle_mod):
+    dev = device()
+    rng = np.random.default_rng([rows, f, k, 8])
+    args, off, d, w = _operands(oracle_mod, rng, dev, rows, f, k, fx, fw, ends)
+    q, s, h = _kept(rng, rows, f)
+    out = tuple(torch.full((rows, n), -77.0, dtype=torch.bfloat16, device=dev) for n in (2 * f, f))
+    dh, y = mx.mx_gated_ffn_backward(*args, to_dev_u8(q, dev), to_dev_u8(s, dev), act="silu", group_end_offsets=off,
+                                     a_format=NAMES[fx], w_format=NAMES[fw], recompute=True, out=out)
+    for i, (lo, hi) in enumerate(r4.bounds(ends, rows)):
+        if hi > lo:
+            _check_backward(dh[lo:hi], y[lo:hi], d[lo:hi], w[i], h[lo:hi], fx, fw, "silu", "group %d" % i)
+    assert bool((dh[hi:] == -77).all()) and bool((y[hi:] == -77).all())
+
+
+@pytest.mark.parametrize("fx,fw", PAIRS)
+def test_large_tiles(fx, fw, oracle_mod):
+    """Enough tiles that the larger ones are taken, with ragged edges."""
+    dev = device()
+    rows, f, k = 4100, 1568, 160
+    rng = np.random.default_rng(11)
+    args, _, x, w = _operands(oracle_mod, rng, dev, rows, 2 * f, k, fx, fw, None)
+    kw = dict(act="silu", a_format=NAMES[fx], w_format=NAMES[fw])
+    y, q, s = mx.mx_gated_ffn(*args, raw=True, **kw)
+    _check_forward(y, q, s, x, w[0], fx, fw, "silu", "large")
+    rows, f, k = 3333, 3680, 96
+    args, _, d, w = _operands(oracle_mod, rng, dev, rows, f, k, fx, fw, None)
+    q, s, h = _kept(rng, rows, f)
+    dh, y = mx.mx_gated_ffn_backward(*args, to_dev_u8(q, dev), to_dev_u8(s, dev), recompute=True, **kw)
+    _check_backward(dh, y, d, w[0], h, fx, fw, "silu", "large")
+
+
+def test_special_sums(oracle_mod):
+    """Blocks of the checkpoint with NaN and Inf sums, and of zeros."""
+    dev = device()
+    rng = np.random.default_rng(12)
+    rows, f, k = 40, 64, 64
+    qx, sx = r4.operand(rng, rows, k, "e2m1", spread=1)
+    qw, sw = r4.operand(rng, 2 * f, k, "e2m1", spread=1)
+    qx[5], sx[6, 0] = 0, 255                   # a row of zeros, a row of NaN
+    sx[7], sw[3] = 250, 250                    # past binary32 where they meet: Inf of either sign, or NaN
+    qx[7], qw[3] = 0x22, 0x22                  # (all ones: +Inf)
+    args = [to_dev_u8(v, dev) for v in (qx, oracle_mod.to_blocked(sx), qw, oracle_mod.to_blocked(sw))]
+    y, q, s = mx.mx_gated_ffn(*args, a_format="mxfp4", w_format="mxfp4", raw=True)
+    q, s = host(q), host(s)
+    assert not q[5].any() and not s[5].any() and bool((y[5] == 0).all())
+    assert np.all(s[6] == 255) and np.all((q[6] & 127) == 127) and bool(torch.isnan(y[6]).all())
+    assert s[7, 0] == 254 and q[7, 3] == 0x7E and s[8, 0] < 255
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_as_its_parts(act, oracle_mod):
+    """The block against the product and the activation one after the other:
+    they differ by the parts' rounding of h to bf16 alone."""
+    dev = device()
+    rng = np.random.default_rng(13)
+    rows, f, k = 150, 96, 256
+    args, _, x, w = _operands(oracle_mod, rng, dev, rows, 2 * f, k, "e4m3", "e4m3", None)
+    y, = mx.mx_gated_ffn(*args, act=act, checkpoint=False)
+    h = mx.mx_gemm_mxfp8(*args)
+    parts, = mx.mx_gated_act(h, act=act, checkpoint=False)
+    hv = _np(h)
+    want = r4.gated(hv, act)
+    mag = r4.product(x, w[0])[1]
+    off = HALF(np.abs(hv)) + 2 * r4.product_error(mag, k, "e4m3", "e4m3")
+    tol = r4.gated_tol(hv, off, act) + 2 * HALF(np.abs(want) + r4.gated_tol(hv, off, act))
+    assert np.all(np.abs(_np(y) - _np(parts)) <= tol)

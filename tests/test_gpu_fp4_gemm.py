@@ -1,0 +1,180 @@
+"""Products with MXFP4 weights on the GPU against binary64, dense and grouped.
+
+Tolerance: tests/fp4_ref.py's product_error on the magnitudes that meet in each
+sum, and the output's one rounding."""
+import numpy as np
+import pytest
+import torch
+
+import fp8_precision_quantization_amd as mx
+from tests import fp4_ref as r4
+from tests import train_ref as ref
+from tests.gpu_util import device, to_dev_u8
+
+pytestmark = pytest.mark.gpu
+
+
+def _np(t):
+    return t.detach().double().cpu().numpy()
+
+
+def _check(got, a, w, fa, k, dt, what):
+    want, mag = r4.product(a, w)
+    tol = r4.product_error(mag, k, fa, "e2m1")
+    ref.assert_close(_np(got), want, r4.round_tol(want, tol, dt == torch.bfloat16), what)
+
+
+# one tile and its edges; odd rows and columns; depths that are not whole
+# stages; both tile sizes (the larger from 192 large tiles on)
+SIZES = [(1, 1, 32), (1, 8, 64), (3, 5, 96), (33, 31, 160), (128, 128, 128), (129, 130, 256), (257, 255, 1056),
+         (64, 1000, 544), (300, 77, 4096), (17, 513, 5120)]
+
+
+@pytest.mark.parametrize("m,n,k", SIZES)
+@pytest.mark.parametrize("fa", ["e2m1", "e4m3"])
+def test_dense(m, n, k, fa, oracle_mod):
+    dev = device()
+    rng = np.random.default_rng([m, n, k, fa == "e2m1"])
+    qa, sa = r4.operand(rng, m, k, fa)
+    qb, sb = r4.operand(rng, n, k, "e2m1")
+    args = [to_dev_u8(v, dev) for v in (qa, oracle_mod.to_blocked(sa), qb, oracle_mod.to_blocked(sb))]
+    a, w = r4.values(qa, sa, fa), r4.values(qb, sb, "e2m1")
+    for dt in (torch.float32, torch.bfloat16):
+        c = mx.mx_gemm_mxfp4(*args, out_dtype=dt)
+        _check(c, a, w, fa, k, dt, "c")
+        assert torch.equal(c, mx.mx_gemm_mxfp4(*args, out_dtype=dt))
+
+
+@pytest.mark.parametrize("m,n,k,fa", [(4097, 3200, 160, "e2m1"), (2049, 6145, 96, "e4m3"), (4096, 3584, 384, "e2m1"),
+                                      (3333, 4000, 416, "e4m3")])
+def test_large_tiles(m, n, k, fa, oracle_mod):
+    """Enough 256 x 256 tiles that these are taken."""
+    dev = device()
+    rng = np.random.default_rng([m, n])
+    qa, sa = r4.operand(rng, m, k, fa)
+    qb, sb = r4.operand(rng, n, k, "e2m1")
+    args = [to_dev_u8(v, dev) for v in (qa, oracle_mod.to_blocked(sa), qb, oracle_mod.to_blocked(sb))]
+    a, w = r4.values(qa, sa, fa), r4.values(qb, sb, "e2m1")
+    for dt in (torch.float32, torch.bfloat16):
+        out = torch.full((m * n + 2,), 7.0, dtype=dt, device=dev)
+        c = mx.mx_gemm_mxfp4(*args, out_dtype=dt, out=out[1:-1].view(m, n))    # at no 16-byte word
+        _check(c, a, w, fa, k, dt, "c")
+        assert out[0] == 7 and out[-1] == 7
+        assert torch.equal(c, mx.mx_gemm_mxfp4(*args, out_dtype=dt))
+
+
+def _grouped(oracle_mod, rng, dev, m, n, k, fa, ends):
+    g = len(ends)
+    qa, sa = r4.operand(rng, m, k, fa)
+    qb, sb = r4.operand(rng, g * n, k, "e2m1")
+    a, w = r4.values(qa, sa, fa), r4.values(qb, sb, "e2m1").reshape(g, n, k)
+    off = np.asarray(ends, np.int32)
+    sa_b, _ = oracle_mod.to_blocked_grouped(sa, off, 0)
+    sb_b = np.stack([oracle_mod.to_blocked(s) for s in sb.reshape(g, n, -1)])
+    args = [to_dev_u8(qa, dev), to_dev_u8(sa_b, dev), to_dev_u8(qb.reshape(g, n, -1), dev), to_dev_u8(sb_b, dev),
+            torch.from_numpy(off).to(dev)]
+    return args, a, w
+
+
+@pytest.mark.parametrize("m,n,k,ends", [
+    (1, 1, 32, [1]), (100, 40, 96, [0, 1, 1, 60, 100]), (700, 200, 416, [130, 130, 514, 690]),
+    (513, 129, 1056, [513, 513, 513]), (64, 300, 160, [10, 5, 64, 70]), (1000, 64, 128, list(range(20, 1001, 20)))])
+@pytest.mark.parametrize("fa", ["e2m1", "e4m3"])
+def test_grouped(m, n, k, ends, fa, oracle_mod):
+    dev = device()
+    rng = np.random.default_rng([m, n, k])
+    args, a, w = _grouped(oracle_mod, rng, dev, m, n, k, fa, ends)
+    for dt in (torch.float32, torch.bfloat16):
+        out = torch.full((m, n), -77.0, dtype=dt, device=dev)
+        c = mx.mx_grouped_gemm_mxfp4(*args, out_dtype=dt, out=out)
+        hi = 0
+        for i, (lo, hi) in enumerate(r4.bounds(ends, m)):
+            if hi > lo:
+                _check(c[lo:hi], a[lo:hi], w[i], fa, k, dt, "group %d" % i)
+        assert bool((c[hi:] == -77).all())    # rows past the last end
+
+
+@pytest.mark.parametrize("fa", ["e2m1", "e4m3"])
+def test_grouped_large_tiles(fa, oracle_mod):
+    dev = device()
+    m, n, k, ends = 6000, 4160, 192, [700, 3000, 3001, 5900]
+    args, a, w = _grouped(oracle_mod, np.random.default_rng(9), dev, m, n, k, fa, ends)
+    c = mx.mx_grouped_gemm_mxfp4(*args, out=torch.full((m, n), -77.0, dtype=torch.bfloat16, device=dev))
+    for i, (lo, hi) in enumerate(r4.bounds(ends, m)):
+        _check(c[lo:hi], a[lo:hi], w[i], fa, k, torch.bfloat16, "group %d" % i)
+    assert bool((c[hi:] == -77).all())
+
+
+@pytest.mark.parametrize("groups", [33, 200])
+def test_many_groups(groups, oracle_mod):
+    dev = device()
+    rng = np.random.default_rng(groups)
+    m, n, k = 777, 48, 64
+    ends = np.sort(rng.integers(0, m + 1, groups))
+    args, a, w = _grouped(oracle_mod, rng, dev, m, n, k, "e2m1", ends)
+    c = mx.mx_grouped_gemm_mxfp4(*args, out_dtype=torch.float32)
+    for i, (lo, hi) in enumerate(r4.bounds(ends, m)):
+        if hi > lo:
+            _check(c[lo:hi], a[lo:hi], w[i], "e2m1", k, torch.float32, "group %d" % i)
+
+
+def test_nan_scales_and_codes(oracle_mod):
+    """A block of scale 0xFF (either side) or an e4m3 NaN code makes its row or
+    column NaN and nothing else; the sign of a code does not matter to it."""
+    dev = device()
+    rng = np.random.default_rng(1)
+    m, n, k = 40, 50, 192
+    for fa in ("e2m1", "e4m3"):
+        qa, sa = r4.operand(rng, m, k, fa)
+        qb, sb = r4.operand(rng, n, k, "e2m1")
+        sa[3, 5], sb[7, 2] = 255, 255
+        if fa == "e4m3":
+            qa[11, 100] = 0xFF
+        args = [to_dev_u8(v, dev) for v in (qa, oracle_mod.to_blocked(sa), qb, oracle_mod.to_blocked(sb))]
+        _check(mx.mx_gemm_mxfp4(*args, out_dtype=torch.float32), r4.values(qa, sa, fa), r4.values(qb, sb, "e2m1"), fa, k,
+               torch.float32, fa)
+
+
+def test_scales_over_their_range(oracle_mod):
+    """Scales of one side large and of the other small, sums in range."""
+    dev = device()
+    rng = np.random.default_rng(2)
+    m, n, k = 65, 66, 224
+    qa, sa = r4.operand(rng, m, k, "e2m1", spread=1)
+    qb, sb = r4.operand(rng, n, k, "e2m1", spread=1)
+    for up in (0, 60, 100, 120):
+        ua, ub = (sa.astype(int) + up).astype(np.uint8), (sb.astype(int) - up).astype(np.uint8)
+        args = [to_dev_u8(v, dev) for v in (qa, oracle_mod.to_blocked(ua), qb, oracle_mod.to_blocked(ub))]
+        _check(mx.mx_gemm_mxfp4(*args, out_dtype=torch.float32), r4.values(qa, ua, "e2m1"), r4.values(qb, ub, "e2m1"),
+               "e2m1", k, torch.float32, "2^%d" % up)
+
+
+def test_empty(oracle_mod):
+    dev = device()
+
+    def z(*shape):
+        return torch.zeros(*shape, dtype=torch.uint8, device=dev)
+
+    assert mx.mx_gemm_mxfp4(z(0, 32), z(0), z(8, 32), z(128, 4)).shape == (0, 8)
+    assert mx.mx_gemm_mxfp4(z(4, 32), z(128, 4), z(0, 32), z(0)).shape == (4, 0)
+    c = mx.mx_gemm_mxfp4(z(4, 0), z(0), z(8, 0), z(0), out=torch.ones(4, 8, dtype=torch.bfloat16, device=dev))
+    assert bool((c == 0).all())
+
+
+def test_as_the_fp8_product(oracle_mod):
+    """The same numbers held in MXFP8 through mx_gemm_mxfp8: the same result up
+    to both sums' bounds."""
+    dev = device()
+    rng = np.random.default_rng(6)
+    m, n, k = 200, 136, 512
+    qb, sb = r4.operand(rng, n, k, "e2m1")
+    qa, sa = r4.operand(rng, m, k, "e4m3")
+    # e2m1 values are e4m3 numbers
+    e4m3 = np.array([0x00, 0x30, 0x38, 0x3C, 0x40, 0x44, 0x48, 0x4C], np.uint8)
+    code = r4.unpack(qb)
+    q8 = e4m3[code & 7] | ((code >> 3) << 7)
+    sa_b, sb_b = to_dev_u8(oracle_mod.to_blocked(sa), dev), to_dev_u8(oracle_mod.to_blocked(sb), dev)
+    four = mx.mx_gemm_mxfp4(to_dev_u8(qa, dev), sa_b, to_dev_u8(qb, dev), sb_b, out_dtype=torch.float32)
+    eight = mx.mx_gemm_mxfp8(to_dev_u8(qa, dev), sa_b, to_dev_u8(q8, dev), sb_b, out_dtype=torch.float32)
+    mag = r4.product(r4.values(qa, sa, "e4m3"), r4.values(qb, sb, "e2m1"))[1]
+    assert np.all(np.abs(_np(four) - _np(eight)) <= 2 * r4.product_error(mag, k, "e4m3", "e2m1"))
