@@ -11,6 +11,7 @@ constexpr int64_t kMaxGridBlocks = (int64_t)UINT32_MAX / 512;   // work-items of
 constexpr int64_t kMaxLd = (int64_t)1 << 31;
 constexpr int64_t kMaxK = (int64_t)1 << 23;             // a tile's row offsets are 32 bits
 constexpr int64_t kMaxWeights = (int64_t)1 << 36;       // a group's scale offsets are 32 bits
+constexpr int64_t kMaxCols = (int64_t)1 << 24;          // and those of 32 rows of a result
 constexpr int64_t kMaxCast = (int64_t)1 << 35;
 
 bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p % a) == 0; }
@@ -40,7 +41,7 @@ bool product_ok(int64_t m, int64_t w_rows, int64_t k, int64_t groups) {
 mx_status gemm(const uint8_t* qa, const uint8_t* sa, int32_t a_format, const uint8_t* qb, const uint8_t* sb,
                const int32_t* ends, int32_t groups, int64_t m, int64_t n, int64_t k, void* c, int32_t c_type,
                hipStream_t stream) {
-  if (!product_ok(m, n, k, groups) || !format_ok(a_format) || !type_ok(c_type))
+  if (!product_ok(m, n, k, groups) || n > kMaxCols || !format_ok(a_format) || !type_ok(c_type))
     return MX_ERR_SHAPE;
   if (m == 0 || n == 0)
     return MX_OK;
@@ -76,7 +77,7 @@ mx_status decode(const void* x, int64_t ldx, const uint8_t* qw, const uint8_t* s
 // The checks that the block and its gradient share; w_rows: of one group.
 mx_status check_ffn(int32_t x_format, int32_t w_format, const int32_t* ends, int32_t groups, int64_t rows,
                     int64_t cols, int64_t w_rows, int64_t k, int32_t act) {
-  if (cols < 0 || cols % MX_BLOCK != 0 || !act_ok(act) || !format_ok(x_format) || !format_ok(w_format) ||
+  if (cols < 0 || cols % MX_BLOCK != 0 || cols > kMaxCols || !act_ok(act) || !format_ok(x_format) || !format_ok(w_format) ||
       (x_format == MX_FORMAT_E2M1 && w_format == MX_FORMAT_E4M3))
     return MX_ERR_SHAPE;
   if (groups < 1 || groups > MX_MAX_GROUPS || (ends == nullptr && groups != 1))
@@ -151,7 +152,7 @@ mx_status mx_gated_ffn_decode(const void* x, int64_t ldx, const uint8_t* qw, con
 mx_status mx_gated_ffn(const uint8_t* qx, const uint8_t* sx, int32_t x_format, const uint8_t* qw, const uint8_t* sw,
                        int32_t w_format, const int32_t* group_end_offsets, int32_t num_groups, int64_t rows,
                        int64_t cols, int64_t k, int32_t act, void* y, uint8_t* q, uint8_t* s, hipStream_t stream) {
-  if (cols >= INT_MAX / 2)
+  if (cols > kMaxCols)
     return MX_ERR_SHAPE;
   const mx_status st = check_ffn(x_format, w_format, group_end_offsets, num_groups, rows, cols, 2 * cols, k, act);
   if (st != MX_OK)

@@ -21,15 +21,15 @@
 // of a row is then two lanes' registers: the epilogues that need a block's
 // largest magnitude exchange it once, and all of them write words.
 //
-// A workgroup of four waves owns a 64 NB x 64 NB tile of R, a wave its
-// quarter in NB x NB blocks.  K advances in stages of 128: the waves bring
-// stage rows (64 bytes of e2m1, 128 of e4m3) and the stage's scales straight
-// from memory into one of kSlots LDS slots, kSlots - 1 stages ahead.  16-byte
-// chunks of a row are permuted by an XOR with bits of the row (through the
-// loads' source offsets, as a load to LDS writes in lane order), so that 16
-// lanes that read one chunk of 16 rows reach all banks.  Operands are read
-// from LDS one 64-deep step ahead of the MFMAs that use them; loads and reads
-// stand between the MFMAs; one barrier a stage.
+// A workgroup of WX x WW waves owns a tile of R, a wave BX x BW blocks of 32 x
+// 32 of it.  K advances in stages of 128: the waves bring stage rows (64 bytes
+// of e2m1, 128 of e4m3) and the stage's scales straight from memory into one
+// of kSlots LDS slots, kSlots - 1 stages ahead.  16-byte chunks of a row are
+// permuted by an XOR with bits of the row (through the loads' source offsets,
+// as a load to LDS writes in lane order), so that 16 lanes that read one chunk
+// of 16 rows reach all banks.  Operands are read from LDS one 64-deep step
+// ahead of the MFMAs that use them; loads and reads stand between the MFMAs;
+// one barrier a stage.
 //
 // Rows past the tile's end, K past the end and whole stages past it load as
 // zeros: their offsets lie outside the buffer's range.
@@ -47,7 +47,6 @@ namespace mx {
 typedef int v8i __attribute__((ext_vector_type(8)));
 typedef float v16f __attribute__((ext_vector_type(16)));
 
-constexpr int kMmThreads = 256;
 constexpr int kMmK = 128;     // K of a stage
 constexpr int kMmBand = 8;    // tile rows to a band of the tile order
 
@@ -66,21 +65,40 @@ __device__ __forceinline__ int mm_swizzle(int row) {
   return CHUNKS == 8 ? (row & 7) ^ ((row >> 3) & 1) : (row >> 2) & 3;
 }
 
-template <int FX, int FW, int NB>
-struct MmTile {
-  static constexpr int kTile = 64 * NB;
+// Tiles.  Large: 256 x 256 by eight waves, two to a SIMD.  Small: 128 x 128 by
+// four, two workgroups to a CU.
+template <bool LARGE>
+struct MmShape;
+template <>
+struct MmShape<true> {
+  static constexpr int kBX = 2, kBW = 4, kWX = 4, kWW = 2, kPerCu = 1;
+};
+template <>
+struct MmShape<false> {
+  static constexpr int kBX = 2, kBW = 2, kWX = 2, kWW = 2, kPerCu = 2;
+};
+
+template <bool LARGE>
+constexpr int kMmThreads = 64 * MmShape<LARGE>::kWX * MmShape<LARGE>::kWW;
+
+template <int FX, int FW, bool LARGE>
+struct MmTile : MmShape<LARGE> {
+  using S = MmShape<LARGE>;
+  static constexpr int kWaves = S::kWX * S::kWW, kThreads = kMmThreads<LARGE>;
+  static constexpr int kRowsX = 32 * S::kBX * S::kWX, kRowsW = 32 * S::kBW * S::kWW;
   static constexpr int kX = 0;
-  static constexpr int kW = kTile * MmFormat<FX>::kRow;
-  static constexpr int kSX = kW + kTile * MmFormat<FW>::kRow;   // scales: 4 bytes a row
-  static constexpr int kSW = kSX + kTile * 4;
-  static constexpr int kSlot = kSW + kTile * 4;
-  // slots that fit 160 KiB, or half of it where two workgroups share a CU
-  static constexpr int kSlots = (NB == 4 ? 163840 : 81920) / kSlot > 4 ? 4 : (NB == 4 ? 163840 : 81920) / kSlot;
+  static constexpr int kW = kRowsX * MmFormat<FX>::kRow;
+  static constexpr int kSX = kW + kRowsW * MmFormat<FW>::kRow;   // scales: 4 bytes a row
+  static constexpr int kSW = kSX + kRowsX * 4;
+  static constexpr int kSlot = kSW + kRowsW * 4;
+  // as many slots as a workgroup's share of a CU's LDS holds, four at most
+  static constexpr int kFit = 163840 / S::kPerCu / kSlot;
+  static constexpr int kSlots = kFit > 4 ? 4 : kFit;
   static constexpr int kLds = kSlots * kSlot;
-  static constexpr int kLoadsX = kTile * MmFormat<FX>::kRow / 4096;   // loads of a wave, 1 KiB each
-  static constexpr int kLoadsW = kTile * MmFormat<FW>::kRow / 4096;
-  static constexpr int kLoadsS = NB == 4 ? 2 : 1;
-  static constexpr int kLoads = kLoadsX + kLoadsW + kLoadsS;
+  static constexpr int kLoadsX = kW / (1024 * kWaves);   // loads of a wave, 1 KiB each
+  static constexpr int kLoadsW = (kSX - kW) / (1024 * kWaves);
+  static constexpr int kLoads = kLoadsX + kLoadsW + 1;   // and 256 bytes of scales
+  static_assert((kRowsX + kRowsW) / 64 == kWaves && kRowsX % 64 == 0, "a wave's scales are one operand's");
   static_assert(kSlots >= 2 && (kSlots - 1) * kLoads < 64, "slots and the load counter");
 };
 
@@ -120,12 +138,6 @@ __device__ __forceinline__ void mm_wave_fence() {
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
   __builtin_amdgcn_wave_barrier();
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-}
-
-// f(0) .. f(N - 1) with the numbers as constants.
-template <class F, int... I>
-__device__ __forceinline__ void mm_each(std::integer_sequence<int, I...>, F f) {
-  (f(std::integral_constant<int, I>()), ...);
 }
 
 // Where a workgroup's tile lies.
@@ -212,19 +224,20 @@ __device__ __forceinline__ bool mm_place(const MmArgs& a, uint8_t* lds, MmPlace&
 }
 
 // The tile's accumulators: acc[i][j] is the block of W rows 32 i and X rows
-// 32 j of this wave's quarter.  GATED: the wave's W rows are 16 NB rows from
-// its columns' gate half and the same of the factor half (n rows on), blocks
-// i < NB / 2 and the others.  col0: the tile's first column of R.
-template <int FX, int FW, int NB, bool GATED>
+// 32 j of this wave's part, wave w's at (w / WW, w % WW).  GATED: the wave's W
+// rows are 16 BW rows from its columns' gate half and the same of the factor
+// half (n rows on), blocks i < BW / 2 and the others.  col0: the tile's first
+// column of R.
+template <int FX, int FW, bool LARGE, bool GATED>
 __device__ __forceinline__ void mm_tile(const MmArgs& a, const MmPlace& p, int64_t col0, uint8_t* lds,
-                                        v16f (&acc)[NB][NB]) {
-  using T = MmTile<FX, FW, NB>;
+                                        v16f (&acc)[MmShape<LARGE>::kBW][MmShape<LARGE>::kBX]) {
+  using T = MmTile<FX, FW, LARGE>;
   using X = MmFormat<FX>;
   using W = MmFormat<FW>;
-  constexpr int kSlots = T::kSlots;
+  constexpr int kSlots = T::kSlots, BX = T::kBX, BW = T::kBW;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wm = wave >> 1, wn = wave & 1;
+  const int wx = wave / T::kWW, ww = wave % T::kWW;
   const int r = lane & 31, h = lane >> 5;
 
   const int ldx = (int)(FX == MX_FORMAT_E2M1 ? a.k / 2 : a.k), ldw = (int)(FW == MX_FORMAT_E2M1 ? a.k / 2 : a.k);
@@ -232,89 +245,77 @@ __device__ __forceinline__ void mm_tile(const MmArgs& a, const MmPlace& p, int64
   const int stages = (int)((a.k + kMmK - 1) / kMmK);
 
   const __amdgpu_buffer_rsrc_t rx = buffer_rsrc(a.qx + p.row0 * ldx, (uint32_t)p.rows * (uint32_t)ldx);
-  const __amdgpu_buffer_rsrc_t rsx =
-      buffer_rsrc(a.sx + p.srow0 / 128 * strip, (uint32_t)((p.rows + 127) / 128 * strip));
   // W: one range, or the gate's and the factor's
-  constexpr int kCols = GATED ? T::kTile / 2 : T::kTile;
+  constexpr int kCols = GATED ? T::kRowsW / 2 : T::kRowsW;
   const int cols = (int)min((int64_t)kCols, a.n - col0);
   const uint8_t* wbase = a.qw + p.group * a.w_bytes + col0 * ldw;
   const __amdgpu_buffer_rsrc_t rw = buffer_rsrc(wbase, (uint32_t)cols * (uint32_t)ldw);
   const __amdgpu_buffer_rsrc_t ru = GATED ? buffer_rsrc(wbase + a.n * ldw, (uint32_t)cols * (uint32_t)ldw) : rw;
-  const int64_t strip0 = col0 / 128;
-  const __amdgpu_buffer_rsrc_t rsw = buffer_rsrc(a.sw + p.group * a.sw_bytes + strip0 * strip,
-                                                 (uint32_t)(a.sw_bytes - strip0 * strip));
 
   const uint32_t lds0 =
       __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds);
 
-  // Loader roles.  Code load u of wave w fills 1 KiB, whole stage rows; the
-  // lane's row of load 0, its chunk of memory, its offset.
-  const int xrow = (64 / X::kChunks) * wave + lane / X::kChunks;
-  const int xchunk = (lane % X::kChunks) ^ mm_swizzle<X::kChunks>(xrow);
-  const uint32_t xoff = xrow * ldx + 16 * xchunk;
-  const int wrow = (64 / W::kChunks) * wave + lane / W::kChunks;
-  const int wchunk = (lane % W::kChunks) ^ mm_swizzle<W::kChunks>(wrow);
-  const uint32_t woff = wrow * ldw + 16 * wchunk;
-  constexpr int kXRows = 4 * 64 / X::kChunks, kWRows = 4 * 64 / W::kChunks;   // rows from load to load
-  // Scales: word d of the stage's is row 32 NB (d / 32 NB) + 32 (d % NB) + d /
-  // NB % 32 of the tile, so that a lane finds its row's words of its NB
-  // blocks together.
-  auto scale_row = [&](int d) { return 32 * NB * (d / (32 * NB)) + 32 * (d % NB) + d / NB % 32; };
-  const int sd = NB == 4 ? threadIdx.x : threadIdx.x & 127;
-  const int srow = scale_row(sd);
-  auto scale_at = [&](int64_t row) {   // of a row of a scale layout, K 0
-    return (uint32_t)(row / 128 * strip + 16 * (row % 32) + 4 * (row % 128 / 32));
-  };
-  const uint32_t sxoff = scale_at(srow);
-  int64_t swrow = col0 % 128 + srow;
-  if constexpr (GATED) {
-    const int half = 16 * NB, quarter = srow / (2 * half), in = srow % (2 * half);
-    swrow = col0 % 128 + half * quarter + in % half + (in >= half ? a.n : 0);
+  // Loader roles.  Code load u of wave w fills 1 KiB: the stage rows from u *
+  // kXRows + w * (64 / chunks) on; the lane's row of them, its chunk of memory.
+  constexpr int kXEach = 64 / X::kChunks, kWEach = 64 / W::kChunks;             // rows of a load
+  constexpr int kXRows = T::kWaves * kXEach, kWRows = T::kWaves * kWEach;       // rows from load to load
+  const int xrow = kXEach * wave, wrow = kWEach * wave;
+  const int xchunk = (lane % X::kChunks) ^ mm_swizzle<X::kChunks>(xrow + lane / X::kChunks);
+  const int wchunk = (lane % W::kChunks) ^ mm_swizzle<W::kChunks>(wrow + lane / W::kChunks);
+  const uint32_t xoff = lane / X::kChunks * ldx + 16 * xchunk, woff = lane / W::kChunks * ldw + 16 * wchunk;
+  // Scales: word d of an operand's stage is row 32 B (d / 32 B) + 32 (d % B) +
+  // d / B % 32 of the tile, B its blocks to a wave, so that a lane finds its
+  // row's words of those blocks together.  The first waves bring X's, the
+  // others W's.
+  const bool s_of_x = wave < T::kRowsX / 64;
+  const int64_t scol0 = col0 / 128 * 128;
+  const __amdgpu_buffer_rsrc_t rs =
+      s_of_x ? buffer_rsrc(a.sx + p.srow0 / 128 * strip, (uint32_t)((p.rows + 127) / 128 * strip))
+             : buffer_rsrc(a.sw + p.group * a.sw_bytes + scol0 / 128 * strip,
+                           (uint32_t)(a.sw_bytes - scol0 / 128 * strip));
+  int64_t srow;   // in the scale layout, from the range's start
+  {
+    const int d = threadIdx.x - (s_of_x ? 0 : T::kRowsX), B = s_of_x ? BX : BW;
+    srow = 32 * B * (d / (32 * B)) + 32 * (d % B) + d / B % 32;
+    if (!s_of_x) {
+      if constexpr (GATED) {
+        constexpr int kHalf = 16 * BW;
+        const int in = (int)srow % (2 * kHalf);
+        srow = (int)srow / (2 * kHalf) * kHalf + in % kHalf + (in >= kHalf ? a.n : 0);
+      }
+      srow += col0 - scol0;
+    }
   }
-  const uint32_t swoff = scale_at(swrow);
+  const uint32_t soff = (uint32_t)(srow / 128 * strip + 16 * (srow % 32) + 4 * (srow % 128 / 32));
 
-  // load i of stage t into slot b: X, W, scales.  Where the tile is 128 high
-  // waves 0 and 1 bring X's scales and the others W's.
+  // load i of stage t into slot b: X, W, scales
   auto load = [&](int i, int t, int b) {
     const uint32_t to = lds0 + b * T::kSlot;
     if (i < T::kLoadsX) {
-      const uint32_t off = (16 * xchunk + t * X::kRow < ldx ? xoff + t * X::kRow : 0x80000000u) + (uint32_t)(i * kXRows * ldx);
-      mm_load<16>(to + T::kX + i * 4096 + wave * 1024, rx, off);
+      const uint32_t off = 16 * xchunk + t * X::kRow < ldx ? xoff + t * X::kRow : 0x80000000u;
+      mm_load<16>(to + T::kX + (i * T::kWaves + wave) * 1024, rx, off + (uint32_t)((i * kXRows + xrow) * ldx));
     } else if (i < T::kLoadsX + T::kLoadsW) {
       const int u = i - T::kLoadsX;
-      // rows of this load: kWRows u on, or in the gate or factor half
-      int rows = u * kWRows;
+      int row = u * kWRows + wrow;
       bool up = false;
       if constexpr (GATED) {
-        constexpr int kHalf = 16 * NB;
-        static_assert(kWRows <= kHalf || kWRows == 2 * kHalf, "a load's rows");
-        if constexpr (kWRows <= kHalf) {
-          up = rows % (2 * kHalf) >= kHalf;
-          rows = rows / (2 * kHalf) * kHalf + rows % kHalf;
-        } else {
-          up = wave >= 2;   // waves 0 and 1 bring the gate's rows, the others the factor's
-          rows = u * kHalf - (up ? kHalf : 0);
-        }
+        constexpr int kHalf = 16 * BW;   // (a multiple of kWEach: a load's rows are of one half)
+        up = row % (2 * kHalf) >= kHalf;
+        row = row / (2 * kHalf) * kHalf + row % kHalf;
       }
-      const uint32_t off = (16 * wchunk + t * W::kRow < ldw ? woff + t * W::kRow : 0x80000000u) + (uint32_t)(rows * ldw);
-      mm_load<16>(to + T::kW + u * 4096 + wave * 1024, GATED && up ? ru : rw, off);
-    } else if constexpr (NB == 4) {
-      if (i == T::kLoads - 2)
-        mm_load<4>(to + T::kSX + wave * 256, rsx, sxoff + t * 512);
-      else
-        mm_load<4>(to + T::kSW + wave * 256, rsw, swoff + t * 512);
+      const uint32_t off = 16 * wchunk + t * W::kRow < ldw ? woff + t * W::kRow : 0x80000000u;
+      mm_load<16>(to + T::kW + (u * T::kWaves + wave) * 1024, GATED && up ? ru : rw, off + (uint32_t)(row * ldw));
     } else {
-      mm_load<4>(to + T::kSX + wave * 256, wave < 2 ? rsx : rsw, (wave < 2 ? sxoff : swoff) + t * 512);
+      mm_load<4>(to + T::kSX + wave * 256, rs, soff + t * 512);
     }
   };
 
   // Operands of a step: [block][word]; and the words of scales of a stage.
-  typedef u32x4 OpX[NB][X::kWords];
-  typedef u32x4 OpW[NB][W::kWords];
-  typedef uint32_t Scales[NB];
-  constexpr int kReads = NB * (X::kWords + W::kWords);
+  typedef u32x4 OpX[BX][X::kWords];
+  typedef u32x4 OpW[BW][W::kWords];
+  constexpr int kReads = BX * X::kWords + BW * W::kWords;
   const int fx = mm_swizzle<X::kChunks>(r), fw = mm_swizzle<W::kChunks>(r);
-  const int xat = T::kX + (wm * 32 * NB + r) * X::kRow, wat = T::kW + (wn * 32 * NB + r) * W::kRow;
+  const int xat = T::kX + (wx * 32 * BX + r) * X::kRow, wat = T::kW + (ww * 32 * BW + r) * W::kRow;
   // read q of step s from slot b: W's first block, X's blocks, W's others
   auto read = [&](int q, int s, int b, OpX& ox, OpW& ow) {
     const uint8_t* slot = lds + b * T::kSlot;
@@ -328,26 +329,23 @@ __device__ __forceinline__ void mm_tile(const MmArgs& a, const MmPlace& p, int64
     };
     if (q < W::kWords)
       one_w(0, q);
-    else if (q < W::kWords + NB * X::kWords)
+    else if (q < W::kWords + BX * X::kWords)
       one_x((q - W::kWords) / X::kWords, (q - W::kWords) % X::kWords);
     else
-      one_w((q - NB * X::kWords) / W::kWords, (q - NB * X::kWords) % W::kWords);
+      one_w((q - BX * X::kWords) / W::kWords, (q - BX * X::kWords) % W::kWords);
   };
-  auto read_scales = [&](int b, Scales& sx, Scales& sw) {
-    const uint8_t* slot = lds + b * T::kSlot;
-    if constexpr (NB == 4) {
-      const u32x4 vx = *reinterpret_cast<const u32x4*>(slot + T::kSX + (wm * 32 + r) * 16);
-      const u32x4 vw = *reinterpret_cast<const u32x4*>(slot + T::kSW + (wn * 32 + r) * 16);
+  auto read_words = [&](const uint8_t* at, auto& s) {
+    constexpr int B = (int)std::extent_v<std::remove_reference_t<decltype(s)>>;
+    typedef uint32_t Words __attribute__((ext_vector_type(B)));
+    const Words v = *reinterpret_cast<const Words*>(at + r * B * 4);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        sx[i] = vx[i], sw[i] = vw[i];
-    } else {
-      const u32x2 vx = *reinterpret_cast<const u32x2*>(slot + T::kSX + (wm * 32 + r) * 8);
-      const u32x2 vw = *reinterpret_cast<const u32x2*>(slot + T::kSW + (wn * 32 + r) * 8);
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        sx[i] = vx[i], sw[i] = vw[i];
-    }
+    for (int i = 0; i < B; ++i)
+      s[i] = v[i];
+  };
+  uint32_t sx[BX], sw[BW], nx[BX], nw[BW];
+  auto read_scales = [&](int b) {
+    read_words(lds + b * T::kSlot + T::kSX + wx * 128 * BX, nx);
+    read_words(lds + b * T::kSlot + T::kSW + ww * 128 * BW, nw);
   };
   auto wide_op = [](const auto& o) {
     if constexpr (std::extent_v<std::remove_reference_t<decltype(o)>> == 2)
@@ -357,17 +355,18 @@ __device__ __forceinline__ void mm_tile(const MmArgs& a, const MmPlace& p, int64
       return (v8i){(int)o[0][0], (int)o[0][1], (int)o[0][2], (int)o[0][3], 0, 0, 0, 0};
   };
   // MFMA q of step s: scale byte 2 s + h of a row's word, h shifted away before
-  auto mfma = [&](auto s_c, int q, const OpX& ox, const OpW& ow, const Scales& sx, const Scales& sw) {
+  constexpr int kMfmas = BX * BW;
+  auto mfma = [&](auto s_c, int q, const OpX& ox, const OpW& ow) {
     constexpr int kByte = 2 * decltype(s_c)::value;
-    const int i = q / NB, j = q % NB;
+    const int i = q / BX, j = q % BX;
     acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wide_op(ow[i]), wide_op(ox[j]), acc[i][j], W::kCode,
                                                                 X::kCode, kByte, (int)sw[i], kByte, (int)sx[j]);
   };
 
 #pragma unroll
-  for (int i = 0; i < NB; ++i)
+  for (int i = 0; i < BW; ++i)
 #pragma unroll
-    for (int j = 0; j < NB; ++j)
+    for (int j = 0; j < BX; ++j)
       acc[i][j] = (v16f){};
   if (stages == 0)
     return;
@@ -381,8 +380,7 @@ __device__ __forceinline__ void mm_tile(const MmArgs& a, const MmPlace& p, int64
   lds_barrier();
   OpX x0, x1;
   OpW w0, w1;
-  Scales sx, sw, nx, nw;
-  read_scales(0, nx, nw);
+  read_scales(0);
 #pragma unroll
   for (int q = 0; q < kReads; ++q)
     read(q, 0, 0, x0, w0);
@@ -391,36 +389,41 @@ __device__ __forceinline__ void mm_tile(const MmArgs& a, const MmPlace& p, int64
   // step's operands.  Then, once this wave's loads of stage t + 1 have landed
   // and every wave has read slot b, the second step: its MFMAs, the loads of
   // stage t + kSlots into slot b and the reads of stage t + 1's first step.
-  constexpr int kMfmas = NB * NB;
+  // The reads stand after the first half of the MFMAs, so that the others
+  // cover their latency.
   using S0 = std::integral_constant<int, 0>;
   using S1 = std::integral_constant<int, 1>;
+  auto reads_by = [](int q) { return min(q * 2 * kReads / kMfmas, kReads); };
   int b = 0;
   for (int t = 0; t < stages; ++t) {
 #pragma unroll
-    for (int i = 0; i < NB; ++i)
-      sx[i] = nx[i] >> (8 * h), sw[i] = nw[i] >> (8 * h);
+    for (int i = 0; i < BW; ++i)
+      sw[i] = nw[i] >> (8 * h);
+#pragma unroll
+    for (int j = 0; j < BX; ++j)
+      sx[j] = nx[j] >> (8 * h);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int q = 0; q < kMfmas; ++q) {
-      mfma(S0(), q, x0, w0, sx, sw);
+      mfma(S0(), q, x0, w0);
 #pragma unroll
-      for (int u = q * kReads / kMfmas; u < (q + 1) * kReads / kMfmas; ++u)
+      for (int u = reads_by(q); u < reads_by(q + 1); ++u)
         read(u, 1, b, x1, w1);
       __builtin_amdgcn_sched_barrier(0);
     }
     mm_wait_loads<(kSlots - 2) * T::kLoads>();
     lds_barrier();
     const int nb = b + 1 == kSlots ? 0 : b + 1;
-    read_scales(nb, nx, nw);
+    read_scales(nb);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int q = 0; q < kMfmas; ++q) {
-      mfma(S1(), q, x1, w1, sx, sw);
+      mfma(S1(), q, x1, w1);
 #pragma unroll
       for (int i = q * T::kLoads / kMfmas; i < (q + 1) * T::kLoads / kMfmas; ++i)
         load(i, t + kSlots, b);
 #pragma unroll
-      for (int u = q * kReads / kMfmas; u < (q + 1) * kReads / kMfmas; ++u)
+      for (int u = reads_by(q); u < reads_by(q + 1); ++u)
         read(u, 0, nb, x0, w0);
       __builtin_amdgcn_sched_barrier(0);
     }
@@ -442,12 +445,12 @@ inline MmArgs mm_args(const MmOperands& in, int64_t m, int64_t n, int64_t w_rows
   return a;
 }
 
-// NB for a result of m rows and n columns: 256 x 256 tiles where they fill
-// the GPU, else 128 x 128.  tile_cols: columns of R that a large tile covers.
-inline int mm_blocks(int64_t m, int64_t n, int32_t groups, int tile_cols) {
+// Whether a result of m rows and n columns is taken in large tiles: where they
+// fill the GPU.  tile_cols: columns of R that a large tile covers.
+inline bool mm_large(int64_t m, int64_t n, int32_t groups, int tile_cols) {
   const int64_t rows = groups > 1 ? m / groups : m;   // (of a group, if they were even)
   const int64_t tiles = (rows + 255) / 256 * (groups > 1 ? groups : 1) * ((n + tile_cols - 1) / tile_cols);
-  return tiles >= 192 ? 4 : 2;
+  return tiles >= 192;
 }
 
 // Tiles of a launch, and its workgroups.  cols_tile: columns of R to a tile.

@@ -69,29 +69,32 @@ __device__ __forceinline__ uint32_t amax32(const v16f& f) {
   return max(s[0], s[1]);
 }
 
-template <int NB, bool GELU>
+template <bool LARGE, bool GELU>
 __device__ __forceinline__ void ffn_store(const MmArgs& a, const FfnArgs& o, const MmPlace& p, int64_t col0,
-                                          uint8_t* lds, const v16f (&acc)[NB][NB]) {
-  constexpr int kCols = 16 * NB;   // of this wave
+                                          uint8_t* lds,
+                                          const v16f (&acc)[MmShape<LARGE>::kBW][MmShape<LARGE>::kBX]) {
+  using S = MmShape<LARGE>;
+  constexpr int kCols = 16 * S::kBW;   // of this wave
   using StageY = Staged<kCols * 2>;
   using StageQ = Staged<kCols>;
   constexpr int kSize = StageY::kSize + 2 * StageQ::kSize;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 31, h = lane >> 5;
+  const int lane = threadIdx.x & 63, r = lane & 31, h = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   uint8_t* mine = lds + wave * kSize;
   const StageY sy = {mine};
   const StageQ sq[2] = {{mine + StageY::kSize}, {mine + StageY::kSize + StageQ::kSize}};
-  const int row0 = (wave >> 1) * 32 * NB;
-  const int64_t c0 = col0 + (wave & 1) * kCols;
+  const int row0 = wave / S::kWW * 32 * S::kBX;
+  const int64_t c0 = col0 + wave % S::kWW * kCols;
   const int n = (int)min((int64_t)kCols, a.n - c0);   // a multiple of 32
 #pragma unroll
-  for (int j = 0; j < NB; ++j) {
+  for (int j = 0; j < S::kBX; ++j) {
     const int rows = p.rows - row0 - 32 * j;
     if (rows <= 0 || n <= 0)
       break;
     const int64_t first = p.row0 + row0 + 32 * j;
 #pragma unroll
-    for (int i = 0; i < NB / 2; ++i) {
-      const v16f &g = acc[i][j], &u = acc[i + NB / 2][j];
+    for (int i = 0; i < S::kBW / 2; ++i) {
+      const v16f &g = acc[i][j], &u = acc[i + S::kBW / 2][j];
 #pragma unroll
       for (int v = 0; v < 16; v += 4) {
         const int col = 32 * i + 2 * v + 4 * h;
@@ -122,154 +125,197 @@ __device__ __forceinline__ void ffn_store(const MmArgs& a, const FfnArgs& o, con
   }
 }
 
-template <int FX, int FW, int NB, bool GROUPED>
-__global__ __launch_bounds__(kMmThreads) __attribute__((amdgpu_waves_per_eu(NB == 4 ? 1 : 2, NB == 4 ? 1 : 2)))
+template <int FX, int FW, bool LARGE, bool GROUPED>
+__global__ __launch_bounds__(kMmThreads<LARGE>) __attribute__((amdgpu_waves_per_eu(2, 2)))
 void ffn_kernel(MmArgs a, FfnArgs o) {
-  using T = MmTile<FX, FW, NB>;
+  using T = MmTile<FX, FW, LARGE>;
   __shared__ __attribute__((aligned(256))) uint8_t lds[T::kLds];
   MmPlace p;
-  if (!mm_place<GROUPED, T::kTile>(a, lds, p))
+  if (!mm_place<GROUPED, T::kRowsX>(a, lds, p))
     return;
-  const int64_t col0 = (int64_t)p.tn * (T::kTile / 2);
-  v16f acc[NB][NB];
-  mm_tile<FX, FW, NB, true>(a, p, col0, lds, acc);
+  const int64_t col0 = (int64_t)p.tn * (T::kRowsW / 2);
+  v16f acc[T::kBW][T::kBX];
+  mm_tile<FX, FW, LARGE, true>(a, p, col0, lds, acc);
   if (o.gelu)
-    ffn_store<NB, true>(a, o, p, col0, lds, acc);
+    ffn_store<LARGE, true>(a, o, p, col0, lds, acc);
   else
-    ffn_store<NB, false>(a, o, p, col0, lds, acc);
+    ffn_store<LARGE, false>(a, o, p, col0, lds, acc);
 }
 
-template <int NB, bool GELU>
+// Backward.  The wave's rows of codes and, after them, of results go through
+// one part of LDS.
+template <bool LARGE, bool GELU>
 __device__ __forceinline__ void ffn_bwd_store(const MmArgs& a, const FfnArgs& o, const MmPlace& p, int64_t col0,
-                                              uint8_t* lds, const v16f (&acc)[NB][NB]) {
-  constexpr int kCols = 32 * NB;
+                                              uint8_t* lds,
+                                              const v16f (&acc)[MmShape<LARGE>::kBW][MmShape<LARGE>::kBX]) {
+  using S = MmShape<LARGE>;
+  constexpr int BW = S::kBW, kCols = 32 * BW;
   using StageQ = Staged<kCols>;
   using StageD = Staged<kCols * 2>;
-  constexpr int kSize = 2 * StageQ::kSize + StageD::kSize;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 31, h = lane >> 5;
+  constexpr int kSize = 2 * StageQ::kSize > StageD::kSize ? 2 * StageQ::kSize : StageD::kSize;
+  const int lane = threadIdx.x & 63, r = lane & 31, h = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   uint8_t* mine = lds + wave * kSize;
   const StageQ sg = {mine}, su = {mine + StageQ::kSize};
-  const StageD sd = {mine + 2 * StageQ::kSize};
-  const int row0 = (wave >> 1) * 32 * NB;
-  const int64_t c0 = col0 + (wave & 1) * kCols;
+  const StageD sd = {mine};
+  const int row0 = wave / S::kWW * 32 * S::kBX;
+  const int64_t c0 = col0 + wave % S::kWW * kCols;
   const int n = (int)min((int64_t)kCols, a.n - c0);   // a multiple of 32
 #pragma unroll
-  for (int j = 0; j < NB; ++j) {
+  for (int j = 0; j < S::kBX; ++j) {
     const int rows = p.rows - row0 - 32 * j;
     if (rows <= 0 || n <= 0)
       break;
     const int64_t first = p.row0 + row0 + 32 * j;
+    // this row's scale bytes and the wave's rows of codes, all on their way at once
     const uint8_t* q = o.q_in + first * 2 * a.n + c0;
-    sg.fill(q, 2 * a.n, rows, n);
-    su.fill(q + a.n, 2 * a.n, rows, n);
-    mm_wave_fence();
-    uint32_t dg[NB][8], du[NB][8], y[NB][8];
+    typename StageQ::Loads lg, lu;
+    StageQ::load(lg, q, 2 * a.n, rows, n);
+    StageQ::load(lu, q + a.n, 2 * a.n, rows, n);
+    const int lds = (int)(a.n / 16);
+    const uint8_t* s = o.s_in + first * lds + c0 / 32;
+    const __amdgpu_buffer_rsrc_t rs = buffer_rsrc(s, (uint32_t)(min(rows, 32) * lds - c0 / 32));
+    float vg[BW], vu[BW];
 #pragma unroll
-    for (int i = 0; i < NB; ++i) {
-      uint32_t bg = 0, bu = 0;
-      if (r < rows && 32 * i < n) {
-        const uint8_t* s = o.s_in + (first + r) * (a.n / 16) + (c0 / 32 + i);
-        bg = s[0], bu = s[a.n / 32];
-      }
-      const float vg = scale_of(bg), vu = scale_of(bu);
-#pragma unroll
-      for (int v = 0; v < 16; v += 4) {
-        const int col = 32 * i + 2 * v + 4 * h;
-        const int cg = (int)sg.template get<uint32_t>(r, col), cu = (int)su.template get<uint32_t>(r, col);
-        const f32x2 g0 = __builtin_amdgcn_cvt_pk_f32_fp8(cg, false), g1 = __builtin_amdgcn_cvt_pk_f32_fp8(cg, true);
-        const f32x2 u0 = __builtin_amdgcn_cvt_pk_f32_fp8(cu, false), u1 = __builtin_amdgcn_cvt_pk_f32_fp8(cu, true);
-        const float g[4] = {g0[0] * vg, g0[1] * vg, g1[0] * vg, g1[1] * vg};
-        const float u[4] = {u0[0] * vu, u0[1] * vu, u1[0] * vu, u1[1] * vu};
-        float fg[4], fu[4], fy[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float s, dt;
-          gate<GELU>(g[e], s, dt);
-          const float dy = acc[i][j][v + e], act = g[e] * s;
-          fu[e] = dy * act;
-          fg[e] = dy * u[e] * (s + dt * s * (1.0f - s));
-          fy[e] = act * u[e];
-        }
-        dg[i][v / 2] = bf16_pair(fg[0], fg[1]), dg[i][v / 2 + 1] = bf16_pair(fg[2], fg[3]);
-        du[i][v / 2] = bf16_pair(fu[0], fu[1]), du[i][v / 2 + 1] = bf16_pair(fu[2], fu[3]);
-        y[i][v / 2] = bf16_pair(fy[0], fy[1]), y[i][v / 2 + 1] = bf16_pair(fy[2], fy[3]);
-      }
+    for (int i = 0; i < BW; ++i) {   // (a block past the columns reads another's byte: it is not stored)
+      vg[i] = scale_of(__builtin_amdgcn_raw_buffer_load_b8(rs, r * lds + i, 0, 0));
+      vu[i] = scale_of(__builtin_amdgcn_raw_buffer_load_b8(rs, r * lds + i + lds / 2, 0, 0));
     }
-    auto leave = [&](const uint32_t (&w)[NB][8], uint16_t* dst, int64_t ld) {
+    sg.place(lg);
+    su.place(lu);
+    mm_wave_fence();
+    uint32_t cg[BW][4], cu[BW][4];
 #pragma unroll
-      for (int i = 0; i < NB; ++i)
+    for (int i = 0; i < BW; ++i)
 #pragma unroll
-        for (int v = 0; v < 16; v += 4)
-          sd.put(r, (32 * i + 2 * v + 4 * h) * 2, (u32x2){w[i][v / 2], w[i][v / 2 + 1]});
+      for (int v = 0; v < 4; ++v) {
+        cg[i][v] = sg.template get<uint32_t>(r, 32 * i + 8 * v + 4 * h);
+        cu[i][v] = su.template get<uint32_t>(r, 32 * i + 8 * v + 4 * h);
+      }
+    mm_wave_fence();
+    // the checkpoint's values of four columns
+    auto four = [](uint32_t c, float scale, float (&f)[4]) {
+      const f32x2 lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)c, false), hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)c, true);
+      f[0] = lo[0] * scale, f[1] = lo[1] * scale, f[2] = hi[0] * scale, f[3] = hi[1] * scale;
+    };
+    auto put = [&](int i, int v, const float (&f)[4]) {
+      sd.put(r, (32 * i + 8 * v + 4 * h) * 2, (u32x2){bf16_pair(f[0], f[1]), bf16_pair(f[2], f[3])});
+    };
+    auto drain = [&](uint16_t* dst, int64_t ld) {
       mm_wave_fence();
       sd.drain(reinterpret_cast<uint8_t*>(dst), ld * 2, rows, n * 2);
       mm_wave_fence();
     };
+    // (block by block: all at once would not fit the registers)
+    u32x2 du[BW][4];
+#pragma unroll
+    for (int i = 0; i < BW; ++i) {
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        float g[4], u[4], fg[4], fu[4];
+        four(cg[i][v], vg[i], g);
+        four(cu[i][v], vu[i], u);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float s, dt;
+          gate<GELU>(g[e], s, dt);
+          const float dy = acc[i][j][4 * v + e];
+          fu[e] = dy * (g[e] * s);
+          fg[e] = dy * u[e] * (s + dt * s * (1.0f - s));
+        }
+        put(i, v, fg);
+        du[i][v] = (u32x2){bf16_pair(fu[0], fu[1]), bf16_pair(fu[2], fu[3])};
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
     uint16_t* dh = o.dh + first * 2 * a.n + c0;
-    leave(dg, dh, 2 * a.n);
-    leave(du, dh + a.n, 2 * a.n);
-    if (o.y != nullptr)
-      leave(y, o.y + first * a.n + c0, a.n);
+    drain(dh, 2 * a.n);
+#pragma unroll
+    for (int i = 0; i < BW; ++i)
+#pragma unroll
+      for (int v = 0; v < 4; ++v)
+        sd.put(r, (32 * i + 8 * v + 4 * h) * 2, du[i][v]);
+    drain(dh + a.n, 2 * a.n);
+    if (o.y != nullptr) {
+#pragma unroll
+      for (int i = 0; i < BW; ++i) {
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          float g[4], u[4], fy[4];
+          // (formed again: kept from above, they would not fit the registers)
+          asm volatile("" : "+v"(cg[i][v]), "+v"(cu[i][v]));
+          four(cg[i][v], vg[i], g);
+          four(cu[i][v], vu[i], u);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            fy[e] = act_of<GELU>(g[e]) * u[e];
+          put(i, v, fy);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      drain(o.y + first * a.n + c0, a.n);
+    }
   }
 }
 
-template <int FX, int FW, int NB, bool GROUPED>
-__global__ __launch_bounds__(kMmThreads) __attribute__((amdgpu_waves_per_eu(NB == 4 ? 1 : 2, NB == 4 ? 1 : 2)))
+template <int FX, int FW, bool LARGE, bool GROUPED>
+__global__ __launch_bounds__(kMmThreads<LARGE>) __attribute__((amdgpu_waves_per_eu(2, 2)))
 void ffn_bwd_kernel(MmArgs a, FfnArgs o) {
-  using T = MmTile<FX, FW, NB>;
+  using T = MmTile<FX, FW, LARGE>;
   __shared__ __attribute__((aligned(256))) uint8_t lds[T::kLds];
-  static_assert(4 * (2 * Staged<32 * NB>::kSize + Staged<64 * NB>::kSize) <= T::kLds, "the epilogue's rows");
+  static_assert(T::kWaves * 2 * Staged<32 * T::kBW>::kSize <= T::kLds &&
+                T::kWaves * Staged<64 * T::kBW>::kSize <= T::kLds, "the epilogue's rows");
   MmPlace p;
-  if (!mm_place<GROUPED, T::kTile>(a, lds, p))
+  if (!mm_place<GROUPED, T::kRowsX>(a, lds, p))
     return;
-  const int64_t col0 = (int64_t)p.tn * T::kTile;
-  v16f acc[NB][NB];
-  mm_tile<FX, FW, NB, false>(a, p, col0, lds, acc);
+  const int64_t col0 = (int64_t)p.tn * T::kRowsW;
+  v16f acc[T::kBW][T::kBX];
+  mm_tile<FX, FW, LARGE, false>(a, p, col0, lds, acc);
   if (o.gelu)
-    ffn_bwd_store<NB, true>(a, o, p, col0, lds, acc);
+    ffn_bwd_store<LARGE, true>(a, o, p, col0, lds, acc);
   else
-    ffn_bwd_store<NB, false>(a, o, p, col0, lds, acc);
+    ffn_bwd_store<LARGE, false>(a, o, p, col0, lds, acc);
 }
 
 static constexpr int32_t E4 = MX_FORMAT_E4M3, E2 = MX_FORMAT_E2M1;
 
-template <int FX, int FW, int NB>
+template <int FX, int FW, bool LARGE>
 static void launch_pair(bool bwd, const MmArgs& a, const FfnArgs& o, dim3 grid, hipStream_t stream) {
-  const dim3 threads(kMmThreads);
+  const dim3 threads(kMmThreads<LARGE>);
   if (bwd) {
     if (a.ends != nullptr)
-      hipLaunchKernelGGL((ffn_bwd_kernel<FX, FW, NB, true>), grid, threads, 0, stream, a, o);
+      hipLaunchKernelGGL((ffn_bwd_kernel<FX, FW, LARGE, true>), grid, threads, 0, stream, a, o);
     else
-      hipLaunchKernelGGL((ffn_bwd_kernel<FX, FW, NB, false>), grid, threads, 0, stream, a, o);
+      hipLaunchKernelGGL((ffn_bwd_kernel<FX, FW, LARGE, false>), grid, threads, 0, stream, a, o);
   } else {
     if (a.ends != nullptr)
-      hipLaunchKernelGGL((ffn_kernel<FX, FW, NB, true>), grid, threads, 0, stream, a, o);
+      hipLaunchKernelGGL((ffn_kernel<FX, FW, LARGE, true>), grid, threads, 0, stream, a, o);
     else
-      hipLaunchKernelGGL((ffn_kernel<FX, FW, NB, false>), grid, threads, 0, stream, a, o);
+      hipLaunchKernelGGL((ffn_kernel<FX, FW, LARGE, false>), grid, threads, 0, stream, a, o);
   }
+}
+
+template <bool LARGE>
+static void launch_formats(bool bwd, int32_t fx, int32_t fw, const MmArgs& a, const FfnArgs& o, dim3 grid,
+                           hipStream_t stream) {
+  if (fx == E2)
+    launch_pair<E2, E2, LARGE>(bwd, a, o, grid, stream);
+  else if (fw == E2)
+    launch_pair<E4, E2, LARGE>(bwd, a, o, grid, stream);
+  else
+    launch_pair<E4, E4, LARGE>(bwd, a, o, grid, stream);
 }
 
 static hipError_t launch_either(bool bwd, const MmOperands& in, int64_t m, int64_t n, int64_t k, const FfnArgs& o,
                                 hipStream_t stream) {
-  const int nb = mm_blocks(m, n, in.groups, bwd ? 256 : 128);
+  const bool large = mm_large(m, n, in.groups, bwd ? 256 : 128);
   MmArgs a = mm_args(in, m, n, bwd ? n : 2 * n, k);
-  const dim3 grid((unsigned)mm_grid(a, 64 * nb, bwd ? 64 * nb : 32 * nb));
-  if (in.x_format == E2) {
-    if (nb == 4)
-      launch_pair<E2, E2, 4>(bwd, a, o, grid, stream);
-    else
-      launch_pair<E2, E2, 2>(bwd, a, o, grid, stream);
-  } else if (in.w_format == E2) {
-    if (nb == 4)
-      launch_pair<E4, E2, 4>(bwd, a, o, grid, stream);
-    else
-      launch_pair<E4, E2, 2>(bwd, a, o, grid, stream);
-  } else {
-    if (nb == 4)
-      launch_pair<E4, E4, 4>(bwd, a, o, grid, stream);
-    else
-      launch_pair<E4, E4, 2>(bwd, a, o, grid, stream);
-  }
+  const int tile = large ? 256 : 128;
+  const dim3 grid((unsigned)mm_grid(a, tile, bwd ? tile : tile / 2));
+  if (large)
+    launch_formats<true>(bwd, in.x_format, in.w_format, a, o, grid, stream);
+  else
+    launch_formats<false>(bwd, in.x_format, in.w_format, a, o, grid, stream);
   return hipGetLastError();
 }
 

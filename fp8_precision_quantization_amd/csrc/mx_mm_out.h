@@ -25,15 +25,26 @@ struct Staged {
   __device__ __forceinline__ V get(int row, int byte) const {
     return *reinterpret_cast<const V*>(at + row * kPitch + byte);
   }
-  // To memory: the first `rows` rows' first `bytes` bytes (a multiple of 16),
-  // rows ld bytes apart, everything 16-byte aligned.
+  // Buffer range and offsets of `rows` rows' first `bytes` bytes (a multiple of
+  // 16), ld apart (32 ld < 2^31): what lies outside is dropped, or read as
+  // zeros, without a branch.
+  static __device__ __forceinline__ __amdgpu_buffer_rsrc_t range(const uint8_t* p, int64_t ld, int rows, int bytes) {
+    return buffer_rsrc(p, (uint32_t)(min(rows, 32) - 1) * (uint32_t)ld + (uint32_t)min(bytes, BYTES));
+  }
+  static __device__ __forceinline__ uint32_t offset(int i, int64_t ld, int bytes, int& row, int& byte) {
+    const int lane = threadIdx.x & 63;
+    row = kRows * i + lane / kLanes, byte = 16 * (lane % kLanes);
+    return byte < bytes ? (uint32_t)row * (uint32_t)ld + (uint32_t)byte : 0x80000000u;
+  }
+  // To memory, everything 16-byte aligned.  POLICY: the stores' cache bits.
+  template <int POLICY = 0>
   __device__ __forceinline__ void drain(uint8_t* dst, int64_t ld, int rows, int bytes) const {
-    const int lane = threadIdx.x & 63, in = lane / kLanes, byte = 16 * (lane % kLanes);
+    const __amdgpu_buffer_rsrc_t rs = range(dst, ld, rows, bytes);
 #pragma unroll
     for (int i = 0; i < 32 / kRows; ++i) {
-      const int row = kRows * i + in;
-      if (row < rows && byte < bytes)
-        __builtin_nontemporal_store(get<u32x4>(row, byte), reinterpret_cast<u32x4*>(dst + row * ld + byte));
+      int row, byte;
+      const uint32_t off = offset(i, ld, bytes, row, byte);
+      __builtin_amdgcn_raw_buffer_store_b128(get<u32x4>(row, byte), rs, off, 0, POLICY);
     }
   }
   // The same in elements of E at any alignment, `n` of them a row.
@@ -44,17 +55,25 @@ struct Staged {
       for (int e = lane; e < min(n, BYTES / (int)sizeof(E)); e += 64)
         dst[row * ld + e] = get<E>(row, e * (int)sizeof(E));
   }
-  // From memory, as drain() writes; zeros elsewhere.
-  __device__ __forceinline__ void fill(const uint8_t* src, int64_t ld, int rows, int bytes) const {
-    const int lane = threadIdx.x & 63, in = lane / kLanes, byte = 16 * (lane % kLanes);
+  // From memory, as drain() writes: the loads, and what they brought to its
+  // place.
+  struct Loads {
+    u32x4 v[32 / kRows];
+  };
+  static __device__ __forceinline__ void load(Loads& w, const uint8_t* src, int64_t ld, int rows, int bytes) {
+    const __amdgpu_buffer_rsrc_t rs = range(src, ld, rows, bytes);
 #pragma unroll
     for (int i = 0; i < 32 / kRows; ++i) {
-      const int row = kRows * i + in;
-      u32x4 v = {0, 0, 0, 0};
-      if (row < rows && byte < bytes)
-        v = *reinterpret_cast<const u32x4*>(src + row * ld + byte);
-      put(row, byte, v);
+      int row, byte;
+      const uint32_t off = offset(i, ld, bytes, row, byte);
+      w.v[i] = __builtin_amdgcn_raw_buffer_load_b128(rs, off, 0, 0);
     }
+  }
+  __device__ __forceinline__ void place(const Loads& w) const {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int i = 0; i < 32 / kRows; ++i)
+      put(kRows * i + lane / kLanes, 16 * (lane % kLanes), w.v[i]);
   }
 };
 

@@ -77,9 +77,9 @@ MX_API mx_status mx_dequantize_mxfp4(const uint8_t* q, const uint8_t* s, int64_t
  * With A in MXFP4 every step of the sum is binary32's; with A in MXFP8 a
  * 64-deep step is summed with less (within 4e-4 of its largest product, as in
  * mx_gemm_mxfp8).  A NaN code or scale gives NaN where it enters.
- * m, n, k >= 0, k % 32 == 0, k <= 2^23, n * k < 2^36, m, n < 2^31 and the
- * tiles of a launch, else MX_ERR_SHAPE; m or n 0 writes nothing; k 0 writes
- * zeros.
+ * m, n, k >= 0, k % 32 == 0, k <= 2^23, n <= 2^24, n * k < 2^36, m < 2^31 and
+ * the tiles of a launch, else MX_ERR_SHAPE; m or n 0 writes nothing; k 0
+ * writes zeros.
  */
 MX_API mx_status mx_gemm_mxfp4(const uint8_t* qa, const uint8_t* sa, int32_t a_format, const uint8_t* qb,
                                const uint8_t* sb, int64_t m, int64_t n, int64_t k, void* c, int32_t c_type,
@@ -129,8 +129,8 @@ MX_API mx_status mx_linear_decode(const void* x, int64_t ldx, const uint8_t* qw,
  *   q, s     the 8-bit checkpoint of (g, u), as mx_gated_act writes it of a
  *            bf16 h, here of the binary32 sums: codes (rows, 2 * cols), 16-byte
  *            aligned, and plain scales (rows, 2 * cols / 32); or both NULL.
- * rows, cols, k >= 0; cols and k multiples of 32; k <= 2^23, 2 * cols * k <
- * 2^36, rows + 256 * num_groups < 2^31, else MX_ERR_SHAPE.
+ * rows, cols, k >= 0; cols and k multiples of 32; k <= 2^23, cols <= 2^24, 2 *
+ * cols * k < 2^36, rows + 256 * num_groups < 2^31, else MX_ERR_SHAPE.
  */
 MX_API mx_status mx_gated_ffn(const uint8_t* qx, const uint8_t* sx, int32_t x_format, const uint8_t* qw,
                               const uint8_t* sw, int32_t w_format, const int32_t* group_end_offsets,
