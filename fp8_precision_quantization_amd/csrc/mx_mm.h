@@ -65,40 +65,29 @@ __device__ __forceinline__ int mm_swizzle(int row) {
   return CHUNKS == 8 ? (row & 7) ^ ((row >> 3) & 1) : (row >> 2) & 3;
 }
 
-// Tiles.  Large: 256 x 256 by eight waves, two to a SIMD.  Small: 128 x 128 by
-// four, two workgroups to a CU.
-template <bool LARGE>
-struct MmShape;
-template <>
-struct MmShape<true> {
-  static constexpr int kBX = 2, kBW = 4, kWX = 4, kWW = 2, kPerCu = 1;
-};
-template <>
-struct MmShape<false> {
-  static constexpr int kBX = 2, kBW = 2, kWX = 2, kWW = 2, kPerCu = 2;
-};
-
-template <bool LARGE>
-constexpr int kMmThreads = 64 * MmShape<LARGE>::kWX * MmShape<LARGE>::kWW;
-
-template <int FX, int FW, bool LARGE>
-struct MmTile : MmShape<LARGE> {
-  using S = MmShape<LARGE>;
-  static constexpr int kWaves = S::kWX * S::kWW, kThreads = kMmThreads<LARGE>;
-  static constexpr int kRowsX = 32 * S::kBX * S::kWX, kRowsW = 32 * S::kBW * S::kWW;
+// Tiles.  Large: 256 x 256, by eight waves, two to a SIMD, or WIDE by four of
+// 128 x 128 each, which read a third less from LDS but leave an epilogue fewer
+// registers.  Small: 128 x 128 by four, two workgroups to a CU.
+template <int FX, int FW, bool LARGE, bool WIDE = false>
+struct MmTile {
+  static constexpr int kBX = WIDE ? 4 : 2, kBW = LARGE ? 4 : 2, kWX = LARGE && !WIDE ? 4 : 2, kWW = 2;
+  static constexpr int kPerCu = LARGE ? 1 : 2, kWavesPerSimd = WIDE ? 1 : 2;
+  static constexpr int kWaves = kWX * kWW, kThreads = 64 * kWaves;
+  static constexpr int kRowsX = 32 * kBX * kWX, kRowsW = 32 * kBW * kWW;
   static constexpr int kX = 0;
   static constexpr int kW = kRowsX * MmFormat<FX>::kRow;
   static constexpr int kSX = kW + kRowsW * MmFormat<FW>::kRow;   // scales: 4 bytes a row
   static constexpr int kSW = kSX + kRowsX * 4;
   static constexpr int kSlot = kSW + kRowsW * 4;
   // as many slots as a workgroup's share of a CU's LDS holds, four at most
-  static constexpr int kFit = 163840 / S::kPerCu / kSlot;
+  static constexpr int kFit = 163840 / kPerCu / kSlot;
   static constexpr int kSlots = kFit > 4 ? 4 : kFit;
   static constexpr int kLds = kSlots * kSlot;
   static constexpr int kLoadsX = kW / (1024 * kWaves);   // loads of a wave, 1 KiB each
   static constexpr int kLoadsW = (kSX - kW) / (1024 * kWaves);
-  static constexpr int kLoads = kLoadsX + kLoadsW + 1;   // and 256 bytes of scales
-  static_assert((kRowsX + kRowsW) / 64 == kWaves && kRowsX % 64 == 0, "a wave's scales are one operand's");
+  static constexpr int kLoadsS = (kRowsX + kRowsW) / 64 / kWaves;   // of scales, 256 bytes each
+  static constexpr int kLoads = kLoadsX + kLoadsW + kLoadsS;
+  static_assert(kLoadsS * kWaves * 64 == kRowsX + kRowsW && kRowsX % 64 == 0, "a load's scales are one operand's");
   static_assert(kSlots >= 2 && (kSlots - 1) * kLoads < 64, "slots and the load counter");
 };
 
@@ -228,10 +217,9 @@ __device__ __forceinline__ bool mm_place(const MmArgs& a, uint8_t* lds, MmPlace&
 // rows are 16 BW rows from its columns' gate half and the same of the factor
 // half (n rows on), blocks i < BW / 2 and the others.  col0: the tile's first
 // column of R.
-template <int FX, int FW, bool LARGE, bool GATED>
+template <int FX, int FW, class T, bool GATED>
 __device__ __forceinline__ void mm_tile(const MmArgs& a, const MmPlace& p, int64_t col0, uint8_t* lds,
-                                        v16f (&acc)[MmShape<LARGE>::kBW][MmShape<LARGE>::kBX]) {
-  using T = MmTile<FX, FW, LARGE>;
+                                        v16f (&acc)[T::kBW][T::kBX]) {
   using X = MmFormat<FX>;
   using W = MmFormat<FW>;
   constexpr int kSlots = T::kSlots, BX = T::kBX, BW = T::kBW;
@@ -265,28 +253,29 @@ __device__ __forceinline__ void mm_tile(const MmArgs& a, const MmPlace& p, int64
   const uint32_t xoff = lane / X::kChunks * ldx + 16 * xchunk, woff = lane / W::kChunks * ldw + 16 * wchunk;
   // Scales: word d of an operand's stage is row 32 B (d / 32 B) + 32 (d % B) +
   // d / B % 32 of the tile, B its blocks to a wave, so that a lane finds its
-  // row's words of those blocks together.  The first waves bring X's, the
-  // others W's.
-  const bool s_of_x = wave < T::kRowsX / 64;
+  // row's words of those blocks together.  Load u of wave w brings words 64 (u
+  // * waves + w) on, X's first.
   const int64_t scol0 = col0 / 128 * 128;
-  const __amdgpu_buffer_rsrc_t rs =
-      s_of_x ? buffer_rsrc(a.sx + p.srow0 / 128 * strip, (uint32_t)((p.rows + 127) / 128 * strip))
-             : buffer_rsrc(a.sw + p.group * a.sw_bytes + scol0 / 128 * strip,
-                           (uint32_t)(a.sw_bytes - scol0 / 128 * strip));
-  int64_t srow;   // in the scale layout, from the range's start
-  {
-    const int d = threadIdx.x - (s_of_x ? 0 : T::kRowsX), B = s_of_x ? BX : BW;
-    srow = 32 * B * (d / (32 * B)) + 32 * (d % B) + d / B % 32;
-    if (!s_of_x) {
+  __amdgpu_buffer_rsrc_t rs[T::kLoadsS];
+  uint32_t soff[T::kLoadsS];
+#pragma unroll
+  for (int u = 0; u < T::kLoadsS; ++u) {
+    const bool of_x = u * T::kWaves + wave < T::kRowsX / 64;
+    rs[u] = of_x ? buffer_rsrc(a.sx + p.srow0 / 128 * strip, (uint32_t)((p.rows + 127) / 128 * strip))
+                 : buffer_rsrc(a.sw + p.group * a.sw_bytes + scol0 / 128 * strip,
+                               (uint32_t)(a.sw_bytes - scol0 / 128 * strip));
+    const int d = threadIdx.x + u * T::kThreads - (of_x ? 0 : T::kRowsX), B = of_x ? BX : BW;
+    int64_t row = 32 * B * (d / (32 * B)) + 32 * (d % B) + d / B % 32;   // in the scale layout, from the range's start
+    if (!of_x) {
       if constexpr (GATED) {
         constexpr int kHalf = 16 * BW;
-        const int in = (int)srow % (2 * kHalf);
-        srow = (int)srow / (2 * kHalf) * kHalf + in % kHalf + (in >= kHalf ? a.n : 0);
+        const int in = (int)row % (2 * kHalf);
+        row = (int)row / (2 * kHalf) * kHalf + in % kHalf + (in >= kHalf ? a.n : 0);
       }
-      srow += col0 - scol0;
+      row += col0 - scol0;
     }
+    soff[u] = (uint32_t)(row / 128 * strip + 16 * (row % 32) + 4 * (row % 128 / 32));
   }
-  const uint32_t soff = (uint32_t)(srow / 128 * strip + 16 * (srow % 32) + 4 * (srow % 128 / 32));
 
   // load i of stage t into slot b: X, W, scales
   auto load = [&](int i, int t, int b) {
@@ -306,7 +295,8 @@ __device__ __forceinline__ void mm_tile(const MmArgs& a, const MmPlace& p, int64
       const uint32_t off = 16 * wchunk + t * W::kRow < ldw ? woff + t * W::kRow : 0x80000000u;
       mm_load<16>(to + T::kW + (u * T::kWaves + wave) * 1024, GATED && up ? ru : rw, off + (uint32_t)(row * ldw));
     } else {
-      mm_load<4>(to + T::kSX + wave * 256, rs, soff + t * 512);
+      const int u = i - T::kLoadsX - T::kLoadsW;
+      mm_load<4>(to + T::kSX + (u * T::kWaves + wave) * 256, rs[u], soff[u] + t * 512);
     }
   };
 
@@ -371,12 +361,15 @@ __device__ __forceinline__ void mm_tile(const MmArgs& a, const MmPlace& p, int64
   if (stages == 0)
     return;
 
+  // A stage's loads are issued in two steps, but with two slots in one (the
+  // second would be late).
+  constexpr int kFirst = kSlots > 2 ? (T::kLoads + 1) / 2 : T::kLoads, kSecond = T::kLoads - kFirst;
 #pragma unroll
   for (int t = 0; t < kSlots; ++t)
 #pragma unroll
-    for (int i = 0; i < T::kLoads; ++i)
+    for (int i = 0; i < (t == kSlots - 1 ? kFirst : T::kLoads); ++i)
       load(i, t, t);
-  mm_wait_loads<(kSlots - 1) * T::kLoads>();
+  mm_wait_loads<(kSlots - 2) * T::kLoads + kFirst>();
   lds_barrier();
   OpX x0, x1;
   OpW w0, w1;
@@ -385,10 +378,11 @@ __device__ __forceinline__ void mm_tile(const MmArgs& a, const MmPlace& p, int64
   for (int q = 0; q < kReads; ++q)
     read(q, 0, 0, x0, w0);
 
-  // Stage t in slot b.  First step: its MFMAs, and the reads of the second
-  // step's operands.  Then, once this wave's loads of stage t + 1 have landed
-  // and every wave has read slot b, the second step: its MFMAs, the loads of
-  // stage t + kSlots into slot b and the reads of stage t + 1's first step.
+  // Stage t in slot b.  First step: its MFMAs, the reads of the second step's
+  // operands and the last loads of stage t + kSlots - 1 into the slot before.
+  // Then, once this wave's loads of stage t + 1 have landed and every wave has
+  // read slot b, the second step: its MFMAs, the first loads of stage t +
+  // kSlots into slot b and the reads of stage t + 1's first step.
   // The reads stand after the first half of the MFMAs, so that the others
   // cover their latency.
   using S0 = std::integral_constant<int, 0>;
@@ -407,6 +401,9 @@ __device__ __forceinline__ void mm_tile(const MmArgs& a, const MmPlace& p, int64
     for (int q = 0; q < kMfmas; ++q) {
       mfma(S0(), q, x0, w0);
 #pragma unroll
+      for (int i = kFirst + q * kSecond / kMfmas; i < kFirst + (q + 1) * kSecond / kMfmas; ++i)
+        load(i, t + kSlots - 1, b == 0 ? kSlots - 1 : b - 1);
+#pragma unroll
       for (int u = reads_by(q); u < reads_by(q + 1); ++u)
         read(u, 1, b, x1, w1);
       __builtin_amdgcn_sched_barrier(0);
@@ -420,7 +417,7 @@ __device__ __forceinline__ void mm_tile(const MmArgs& a, const MmPlace& p, int64
     for (int q = 0; q < kMfmas; ++q) {
       mfma(S1(), q, x1, w1);
 #pragma unroll
-      for (int i = q * T::kLoads / kMfmas; i < (q + 1) * T::kLoads / kMfmas; ++i)
+      for (int i = q * kFirst / kMfmas; i < (q + 1) * kFirst / kMfmas; ++i)
         load(i, t + kSlots, b);
 #pragma unroll
       for (int u = reads_by(q); u < reads_by(q + 1); ++u)

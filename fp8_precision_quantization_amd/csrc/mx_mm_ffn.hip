@@ -69,11 +69,10 @@ __device__ __forceinline__ uint32_t amax32(const v16f& f) {
   return max(s[0], s[1]);
 }
 
-template <bool LARGE, bool GELU>
+template <class S, bool GELU>
 __device__ __forceinline__ void ffn_store(const MmArgs& a, const FfnArgs& o, const MmPlace& p, int64_t col0,
                                           uint8_t* lds,
-                                          const v16f (&acc)[MmShape<LARGE>::kBW][MmShape<LARGE>::kBX]) {
-  using S = MmShape<LARGE>;
+                                          const v16f (&acc)[S::kBW][S::kBX]) {
   constexpr int kCols = 16 * S::kBW;   // of this wave
   using StageY = Staged<kCols * 2>;
   using StageQ = Staged<kCols>;
@@ -126,7 +125,7 @@ __device__ __forceinline__ void ffn_store(const MmArgs& a, const FfnArgs& o, con
 }
 
 template <int FX, int FW, bool LARGE, bool GROUPED>
-__global__ __launch_bounds__(kMmThreads<LARGE>) __attribute__((amdgpu_waves_per_eu(2, 2)))
+__global__ __launch_bounds__(LARGE ? 512 : 256) __attribute__((amdgpu_waves_per_eu(2, 2)))
 void ffn_kernel(MmArgs a, FfnArgs o) {
   using T = MmTile<FX, FW, LARGE>;
   __shared__ __attribute__((aligned(256))) uint8_t lds[T::kLds];
@@ -135,20 +134,19 @@ void ffn_kernel(MmArgs a, FfnArgs o) {
     return;
   const int64_t col0 = (int64_t)p.tn * (T::kRowsW / 2);
   v16f acc[T::kBW][T::kBX];
-  mm_tile<FX, FW, LARGE, true>(a, p, col0, lds, acc);
+  mm_tile<FX, FW, T, true>(a, p, col0, lds, acc);
   if (o.gelu)
-    ffn_store<LARGE, true>(a, o, p, col0, lds, acc);
+    ffn_store<T, true>(a, o, p, col0, lds, acc);
   else
-    ffn_store<LARGE, false>(a, o, p, col0, lds, acc);
+    ffn_store<T, false>(a, o, p, col0, lds, acc);
 }
 
 // Backward.  The wave's rows of codes and, after them, of results go through
 // one part of LDS.
-template <bool LARGE, bool GELU>
+template <class S, bool GELU>
 __device__ __forceinline__ void ffn_bwd_store(const MmArgs& a, const FfnArgs& o, const MmPlace& p, int64_t col0,
                                               uint8_t* lds,
-                                              const v16f (&acc)[MmShape<LARGE>::kBW][MmShape<LARGE>::kBX]) {
-  using S = MmShape<LARGE>;
+                                              const v16f (&acc)[S::kBW][S::kBX]) {
   constexpr int BW = S::kBW, kCols = 32 * BW;
   using StageQ = Staged<kCols>;
   using StageD = Staged<kCols * 2>;
@@ -259,7 +257,7 @@ __device__ __forceinline__ void ffn_bwd_store(const MmArgs& a, const FfnArgs& o,
 }
 
 template <int FX, int FW, bool LARGE, bool GROUPED>
-__global__ __launch_bounds__(kMmThreads<LARGE>) __attribute__((amdgpu_waves_per_eu(2, 2)))
+__global__ __launch_bounds__(LARGE ? 512 : 256) __attribute__((amdgpu_waves_per_eu(2, 2)))
 void ffn_bwd_kernel(MmArgs a, FfnArgs o) {
   using T = MmTile<FX, FW, LARGE>;
   __shared__ __attribute__((aligned(256))) uint8_t lds[T::kLds];
@@ -270,18 +268,18 @@ void ffn_bwd_kernel(MmArgs a, FfnArgs o) {
     return;
   const int64_t col0 = (int64_t)p.tn * T::kRowsW;
   v16f acc[T::kBW][T::kBX];
-  mm_tile<FX, FW, LARGE, false>(a, p, col0, lds, acc);
+  mm_tile<FX, FW, T, false>(a, p, col0, lds, acc);
   if (o.gelu)
-    ffn_bwd_store<LARGE, true>(a, o, p, col0, lds, acc);
+    ffn_bwd_store<T, true>(a, o, p, col0, lds, acc);
   else
-    ffn_bwd_store<LARGE, false>(a, o, p, col0, lds, acc);
+    ffn_bwd_store<T, false>(a, o, p, col0, lds, acc);
 }
 
 static constexpr int32_t E4 = MX_FORMAT_E4M3, E2 = MX_FORMAT_E2M1;
 
 template <int FX, int FW, bool LARGE>
 static void launch_pair(bool bwd, const MmArgs& a, const FfnArgs& o, dim3 grid, hipStream_t stream) {
-  const dim3 threads(kMmThreads<LARGE>);
+  const dim3 threads(MmTile<FX, FW, LARGE>::kThreads);
   if (bwd) {
     if (a.ends != nullptr)
       hipLaunchKernelGGL((ffn_bwd_kernel<FX, FW, LARGE, true>), grid, threads, 0, stream, a, o);

@@ -11,10 +11,9 @@ struct MmGemmOut {
   bool f32, words;   // binary32 or bf16; rows of whole 16-byte words
 };
 
-template <bool LARGE, class E>
+template <class S, class E>
 __device__ __forceinline__ void store_c(const MmArgs& a, const MmPlace& p, int64_t col0, uint8_t* lds, bool words,
-                                        E* c, const v16f (&acc)[MmShape<LARGE>::kBW][MmShape<LARGE>::kBX]) {
-  using S = MmShape<LARGE>;
+                                        E* c, const v16f (&acc)[S::kBW][S::kBX]) {
   using Stage = Staged<32 * S::kBW * (int)sizeof(E)>;
   const int lane = threadIdx.x & 63, r = lane & 31, h = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -48,10 +47,13 @@ __device__ __forceinline__ void store_c(const MmArgs& a, const MmPlace& p, int64
   }
 }
 
+template <int FX, bool LARGE>
+using GemmTile = MmTile<FX, MX_FORMAT_E2M1, LARGE, LARGE>;
+
 template <int FX, bool LARGE, bool GROUPED>
-__global__ __launch_bounds__(kMmThreads<LARGE>) __attribute__((amdgpu_waves_per_eu(2, 2)))
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(LARGE ? 1 : 2, LARGE ? 1 : 2)))
 void mm_gemm_kernel(MmArgs a, MmGemmOut o) {
-  using T = MmTile<FX, MX_FORMAT_E2M1, LARGE>;
+  using T = GemmTile<FX, LARGE>;
   __shared__ __attribute__((aligned(256))) uint8_t lds[T::kLds];
   static_assert(T::kWaves * Staged<128 * T::kBW>::kSize <= T::kLds, "the epilogue's rows");
   MmPlace p;
@@ -59,16 +61,16 @@ void mm_gemm_kernel(MmArgs a, MmGemmOut o) {
     return;
   const int64_t col0 = (int64_t)p.tn * T::kRowsW;
   v16f acc[T::kBW][T::kBX];
-  mm_tile<FX, MX_FORMAT_E2M1, LARGE, false>(a, p, col0, lds, acc);
+  mm_tile<FX, MX_FORMAT_E2M1, T, false>(a, p, col0, lds, acc);
   if (o.f32)
-    store_c<LARGE>(a, p, col0, lds, o.words, static_cast<float*>(o.c), acc);
+    store_c<T>(a, p, col0, lds, o.words, static_cast<float*>(o.c), acc);
   else
-    store_c<LARGE>(a, p, col0, lds, o.words, static_cast<uint16_t*>(o.c), acc);
+    store_c<T>(a, p, col0, lds, o.words, static_cast<uint16_t*>(o.c), acc);
 }
 
 template <int FX, bool LARGE>
 static void launch(const MmArgs& a, const MmGemmOut& o, dim3 grid, hipStream_t stream) {
-  const dim3 threads(kMmThreads<LARGE>);
+  const dim3 threads(GemmTile<FX, LARGE>::kThreads);
   if (a.ends != nullptr)
     hipLaunchKernelGGL((mm_gemm_kernel<FX, LARGE, true>), grid, threads, 0, stream, a, o);
   else
