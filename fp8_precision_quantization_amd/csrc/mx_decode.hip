@@ -2,27 +2,31 @@
 //   y[t][j] = sum over k of x[t][k] * W(j, k), or with W's rows a gate and a
 //   factor half, y = act(x Wg^T) (x Wu^T).
 //
-// Bound by the weights' bytes, and for one projection of a layer by latency.
 // Codes become bf16 in registers (exactly, but where 2^e leaves bf16's range)
 // and meet x in v_mfma_f32_16x16x32_bf16: x is not rounded, and sums are
-// binary32.  A lane holds one block of 32 of K of one row of W, a quarter of a
-// 128-deep chunk: its 16 or 32 bytes of codes are one or two loads, all of one
-// scale.  The four MFMAs of a chunk take 8 of a lane's 32 elements each, of W
-// and of x alike: the order of K inside a sum is free.
+// binary32.  A chunk is 128 of K, four blocks and four MFMAs.  A lane holds one
+// block of one row of W, its 16 or 32 bytes of codes under one scale, and MFMA u
+// takes elements 8 u .. + 7 of every lane's block, of W and of x alike: the
+// order of K inside a sum is free.
 //
-// A workgroup owns 16 RB columns (of each half) and its waves take chunks of K
-// in turn; their sums meet in LDS in a fixed order.
+// Bound by the weights' bytes for a row or two of x, and then by x itself, which
+// every workgroup reads.  Lanes of a load should be neighbours in memory (a load
+// whose neighbouring lanes are 16 different rows moves a quarter of the bytes a
+// cycle), while the MFMAs want 16 rows in neighbouring lanes: rows go straight
+// from memory to LDS, whole 64-byte lines and more at a time, 16-byte pieces
+// permuted by an XOR with the row so that the reads meet no bank twice.
+//
+// A workgroup owns 16 RB columns (of each half); its waves take chunks of K in
+// turn, each through BUFS buffers of its own without any barrier, and their sums
+// meet in LDS in a fixed order.
 #include "mx_fp4_launch.h"
 #include "mx_gate.h"
+#include "mx_mm.h"
 #include "mx_train.h"
-#include "mxfp4.h"
 
 namespace mx {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-
-constexpr int kDecodeWaves = 8;
-constexpr int kDecodeThreads = 64 * kDecodeWaves;
 
 struct DecodeArgs {
   const uint16_t* x;
@@ -34,35 +38,70 @@ struct DecodeArgs {
   bool f32, gelu;
 };
 
-struct __attribute__((packed, aligned(2))) AnyWord {
-  u32x4 v;
+// FW: codes of W; TB: blocks of 16 rows of x; KS: waves.
+template <int FW, int TB, int RB, bool GATED>
+struct DecodeBuffer {
+  static constexpr int kRows = GATED ? 2 * RB : RB;                       // blocks of 16 rows of W
+  static constexpr int kRow = FW == MX_FORMAT_E2M1 ? 64 : 128;            // bytes of a chunk of one
+  static constexpr int kX = 0, kW = TB * 4096, kS = kW + kRows * 16 * kRow;
+  static constexpr int kBytes = kS + 256;
+  static constexpr int kLoadsW = kRows * kRow / 64, kLoads = TB * 4 + kLoadsW + 1;
+  static_assert(kRows <= 4, "scales of 64 rows");
 };
 
-// FW: codes of W; TB: blocks of 16 rows of x; RB: blocks of 16 columns.
-template <int FW, int TB, int RB, bool GATED>
-__global__ __launch_bounds__(kDecodeThreads) void decode_kernel(DecodeArgs a) {
+template <int FW, int TB, int RB, int KS, int BUFS, bool GATED>
+__global__ __launch_bounds__(64 * KS) void decode_kernel(DecodeArgs a) {
+  using B = DecodeBuffer<FW, TB, RB, GATED>;
   constexpr bool kFp4 = FW == MX_FORMAT_E2M1;
-  constexpr int kWords = kFp4 ? 1 : 2;
-  constexpr int kRows = GATED ? 2 * RB : RB;   // blocks of 16 rows of W
-  __shared__ float sums[kDecodeWaves][kRows][TB][4][64];
+  constexpr int kRows = B::kRows, kPieces = B::kRow / 16, kWords = kFp4 ? 1 : 2;
+  static_assert(128 % (16 * RB) == 0, "a workgroup's rows lie in one strip of a scale layout");
+  constexpr int kSums = KS * kRows * TB * 1024;
+  constexpr int kLds = KS * BUFS * B::kBytes > kSums ? KS * BUFS * B::kBytes : kSums;
+  static_assert((BUFS - 1) * B::kLoads < 64 && kLds <= 163840, "the load counter and LDS");
+  __shared__ __attribute__((aligned(256))) uint8_t lds[kLds];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 15, q = lane >> 4;
   const int64_t j0 = (int64_t)blockIdx.x * 16 * RB;
-  const int64_t ldw = kFp4 ? a.k / 2 : a.k, strip = (a.k / 32 + 3) / 4 * 512;
-  const int32_t blocks = (int32_t)(a.k / 32), chunks = (blocks + 3) / 4;
+  const int ldw = (int)(kFp4 ? a.k / 2 : a.k), strip = (int)((a.k / 32 + 3) / 4) * 512;
+  const int chunks = (int)((a.k + 127) / 128);
 
-  const uint8_t *w[kRows], *s[kRows];
-#pragma unroll
-  for (int i = 0; i < kRows; ++i) {
-    // a row past the end reads the last one's bytes and is not stored
-    const int64_t j = min(j0 + 16 * (i % RB) + c, a.n - 1) + (i >= RB ? a.n : 0);
-    w[i] = a.qw + j * ldw + 16 * kWords * q;
-    s[i] = a.sw + j / 128 * strip + 16 * (j % 32) + 4 * (j % 128 / 32) + q;
+  // Ranges over the workgroup's rows of each half of W and all of x: rows past
+  // the end, and K past it (an offset outside), read as zeros.
+  const int64_t rows = min((int64_t)16 * RB, a.n - j0), up = GATED ? a.n : 0;
+  const __amdgpu_buffer_rsrc_t rw = buffer_rsrc(a.qw + j0 * ldw, (uint32_t)(rows * ldw));
+  const __amdgpu_buffer_rsrc_t ru = GATED ? buffer_rsrc(a.qw + (j0 + up) * ldw, (uint32_t)(rows * ldw)) : rw;
+  const __amdgpu_buffer_rsrc_t rx = buffer_rsrc(a.x, (uint32_t)(((a.m - 1) * a.ldx + a.k) * 2));
+  // scale words: lane l's is of W's row l of the workgroup's, gate's rows first
+  const int64_t srow0 = j0 / 128 * 128, srows = (a.n + up + 127) / 128 * 128 - srow0;
+  const __amdgpu_buffer_rsrc_t rs = buffer_rsrc(a.sw + srow0 / 128 * strip, (uint32_t)(srows / 128 * strip));
+  uint32_t soff;
+  {
+    const int64_t row = j0 - srow0 + lane % (16 * RB) + (lane >= 16 * RB ? up : 0);
+    soff = lane < 16 * kRows ? (uint32_t)(row / 128 * strip + 16 * (row % 32) + 4 * (row % 128 / 32)) : 0x80000000u;
   }
-  const uint16_t* x[TB];
+  // x: load u brings rows 4 u .. + 3, a lane piece l % 16 ^ row % 16 of its
+  // row; W: 64 / kPieces rows
+  const int xrow = lane / 16, wrow = lane / kPieces;
+  const uint32_t mine =
+      __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds) +
+      wave * BUFS * B::kBytes;
+  auto load = [&](int ch, int b) {
+    const uint32_t to = mine + b * B::kBytes;
 #pragma unroll
-  for (int t = 0; t < TB; ++t)
-    x[t] = a.x + min(16 * t + c, a.m - 1) * a.ldx + 32 * q;
+    for (int u = 0; u < TB * 4; ++u) {
+      const int row = 4 * u + xrow, k = 128 * ch + 8 * ((lane % 16) ^ (row % 16));
+      mm_load<16>(to + B::kX + u * 1024, rx,
+                  row < a.m && k < a.k ? ((uint32_t)row * (uint32_t)a.ldx + k) * 2 : 0x80000000u);
+    }
+#pragma unroll
+    for (int u = 0; u < B::kLoadsW; ++u) {
+      constexpr int kEach = 64 / kPieces, kHalf = 16 * RB;
+      const int row = u * kEach + wrow, byte = ch * B::kRow + 16 * ((lane % kPieces) ^ mm_swizzle<kPieces>(row));
+      mm_load<16>(to + B::kW + u * 1024, u * kEach < kHalf ? rw : ru,
+                  byte < ldw ? (uint32_t)(row % kHalf * ldw + byte) : 0x80000000u);
+    }
+    mm_load<4>(to + B::kS, rs, soff + ch * 512);
+  };
 
   f32x4 acc[kRows][TB];
 #pragma unroll
@@ -70,72 +109,84 @@ __global__ __launch_bounds__(kDecodeThreads) void decode_kernel(DecodeArgs a) {
 #pragma unroll
     for (int t = 0; t < TB; ++t)
       acc[i][t] = (f32x4){};
-
-  for (int ch = wave; ch < chunks; ch += kDecodeWaves) {
-    const bool on = 4 * ch + q < blocks;
-    u32x4 wq[kRows][kWords], xv[TB][4];
-    uint32_t sb[kRows];
+  auto multiply = [&](int b) {
+    const uint8_t* at = lds + (wave * BUFS + b) * B::kBytes;
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
-      sb[i] = on ? s[i][(int64_t)ch * 512] : 127u;
+      u32x4 w[kWords];
 #pragma unroll
-      for (int u = 0; u < kWords; ++u)
-        wq[i][u] = on ? reinterpret_cast<const u32x4*>(w[i] + (int64_t)ch * 64 * kWords)[u] : (u32x4){0, 0, 0, 0};
-    }
-#pragma unroll
-    for (int t = 0; t < TB; ++t)
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-        xv[t][u] = on ? reinterpret_cast<const AnyWord*>(x[t] + (int64_t)ch * 128 + 8 * u)->v : (u32x4){0, 0, 0, 0};
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      const float scale = __uint_as_float(sb[i] << 23);
+      for (int v = 0; v < kWords; ++v)
+        w[v] = *reinterpret_cast<const u32x4*>(at + B::kW + (16 * i + c) * B::kRow +
+                                               16 * ((kWords * q + v) ^ mm_swizzle<kPieces>(c)));
+      const uint32_t byte = at[B::kS + 4 * (16 * i + c) + q];
+      const float scale = __uint_as_float(byte << 23);
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         uint32_t f[4];
         if constexpr (kFp4) {
-          f[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(wq[i][0][u], scale, 0));
-          f[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(wq[i][0][u], scale, 1));
-          f[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(wq[i][0][u], scale, 2));
-          f[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(wq[i][0][u], scale, 3));
+          f[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[0][u], scale, 0));
+          f[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[0][u], scale, 1));
+          f[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[0][u], scale, 2));
+          f[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[0][u], scale, 3));
         } else {
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const uint32_t d = wq[i][u / 2][2 * (u % 2) + e];
-            f[2 * e] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(d, scale, false));
-            f[2 * e + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(d, scale, true));
+          for (int v = 0; v < 2; ++v) {
+            const uint32_t d = w[u / 2][2 * (u % 2) + v];
+            f[2 * v] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(d, scale, false));
+            f[2 * v + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(d, scale, true));
           }
         }
         // a NaN block (the convert knows no scale 0xFF)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          f[e] = sb[i] == 0xFF ? 0x7FC07FC0u : f[e];
+          f[e] = byte == 0xFF ? 0x7FC07FC0u : f[e];
         const bf16x8 wf = __builtin_bit_cast(bf16x8, (u32x4){f[0], f[1], f[2], f[3]});
 #pragma unroll
-        for (int t = 0; t < TB; ++t)
-          acc[i][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf, __builtin_bit_cast(bf16x8, xv[t][u]), acc[i][t], 0, 0, 0);
+        for (int t = 0; t < TB; ++t) {
+          const u32x4 x = *reinterpret_cast<const u32x4*>(at + B::kX + (16 * t + c) * 256 + 16 * ((4 * q + u) ^ c));
+          acc[i][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf, __builtin_bit_cast(bf16x8, x), acc[i][t], 0, 0, 0);
+        }
       }
     }
+  };
+  // The wave's chunks are wave + KS i.  Every turn issues a chunk's loads (past
+  // K they bring zeros), so that one count of loads tells when a chunk is there.
+#pragma unroll
+  for (int i = 0; i < BUFS - 1; ++i)
+    load(wave + KS * i, i);
+  int b = 0;
+  for (int ch = wave; ch < chunks; ch += KS) {
+    load(ch + KS * (BUFS - 1), b == 0 ? BUFS - 1 : b - 1);
+    mm_wait_loads<(BUFS - 1) * B::kLoads>();
+    mm_wave_fence();
+    multiply(b);
+    mm_wave_fence();
+    __builtin_amdgcn_s_waitcnt(0xC07F);   // its reads are done (lgkmcnt 0) before the buffer is loaded again
+    b = b + 1 == BUFS ? 0 : b + 1;
   }
+  mm_wait_loads<0>();
+  __syncthreads();
 
   // Register v of lane l: column 4 (l / 16) + v, row l % 16 of its block.
+  float* sums = reinterpret_cast<float*>(lds);   // [wave][block][block of x][v][lane]
+  auto sum_at = [](int u, int i, int t, int v, int l) { return (((u * kRows + i) * TB + t) * 4 + v) * 64 + l; };
 #pragma unroll
   for (int i = 0; i < kRows; ++i)
 #pragma unroll
     for (int t = 0; t < TB; ++t)
 #pragma unroll
       for (int v = 0; v < 4; ++v)
-        sums[wave][i][t][v][lane] = acc[i][t][v];
+        sums[sum_at(wave, i, t, v, lane)] = acc[i][t][v];
   __syncthreads();
   auto total = [&](int i, int t, int v, int l) {
     float f = 0.0f;
 #pragma unroll
-    for (int u = 0; u < kDecodeWaves; ++u)
-      f += sums[u][i][t][v][l];
+    for (int u = 0; u < KS; ++u)
+      f += sums[sum_at(u, i, t, v, l)];
     return f;
   };
   // element e of the workgroup's 16 TB rows of 16 RB columns
-  for (int e = threadIdx.x; e < 256 * TB * RB; e += kDecodeThreads) {
+  for (int e = threadIdx.x; e < 256 * TB * RB; e += 64 * KS) {
     const int row = e / (16 * RB), col = e % (16 * RB);
     if (row >= a.m || j0 + col >= a.n)
       continue;
@@ -153,32 +204,40 @@ __global__ __launch_bounds__(kDecodeThreads) void decode_kernel(DecodeArgs a) {
   }
 }
 
-template <int FW, int TB, int RB>
-static void launch(const DecodeArgs& a, bool gated, hipStream_t stream) {
-  const dim3 grid((unsigned)((a.n + 16 * RB - 1) / (16 * RB))), threads(kDecodeThreads);
-  if (gated)
-    hipLaunchKernelGGL((decode_kernel<FW, TB, RB, true>), grid, threads, 0, stream, a);
-  else
-    hipLaunchKernelGGL((decode_kernel<FW, TB, RB, false>), grid, threads, 0, stream, a);
+// Two blocks of 16 rows of W to a workgroup (half the reads of x that one
+// makes), two buffers to a wave, eight waves or as many as LDS holds.  Timed
+// (MXFP4, us): 1 x 8192 x 5120 6.7 (one block 8.1, four waves 7.2, four blocks
+// 7.9), 32 x 8192 x 5120 9.7 (one block 14.6, three buffers 10.0), 33 x 5120 x
+// 8192 15.9 (one block 25.7, two waves 22), 64 x 5120 x 8192 19.8 (two waves
+// 33).
+template <int FW, int TB, bool GATED>
+static void launch(const DecodeArgs& a, hipStream_t stream) {
+  constexpr int RB = GATED ? 1 : 2, kBufs = 2;
+  constexpr int kFit = 163840 / (kBufs * DecodeBuffer<FW, TB, RB, GATED>::kBytes);
+  constexpr int KS = TB == 1 && kFit >= 8 ? 8 : kFit >= 4 ? 4 : kFit;
+  hipLaunchKernelGGL((decode_kernel<FW, TB, RB, KS, kBufs, GATED>), dim3((unsigned)((a.n + 16 * RB - 1) / (16 * RB))),
+                     dim3(64 * KS), 0, stream, a);
 }
 
-template <int FW>
-static void launch_rows(const DecodeArgs& a, bool gated, hipStream_t stream) {
+template <int FW, bool GATED>
+static void launch_rows(const DecodeArgs& a, hipStream_t stream) {
   if (a.m <= 16)
-    launch<FW, 1, 1>(a, gated, stream);
+    launch<FW, 1, GATED>(a, stream);
   else if (a.m <= 32)
-    launch<FW, 2, 1>(a, gated, stream);
+    launch<FW, 2, GATED>(a, stream);
+  else if (a.m <= 48)
+    launch<FW, 3, GATED>(a, stream);
   else
-    launch<FW, 4, 1>(a, gated, stream);
+    launch<FW, 4, GATED>(a, stream);
 }
 
 hipError_t launch_decode(const void* x, int64_t ldx, const uint8_t* qw, const uint8_t* sw, int32_t w_format, int64_t m,
                          int64_t n, int64_t k, bool gated, bool gelu, void* c, bool f32, hipStream_t stream) {
   const DecodeArgs a = {static_cast<const uint16_t*>(x), ldx, qw, sw, n, k, (int32_t)m, c, f32, gelu};
   if (w_format == MX_FORMAT_E2M1)
-    launch_rows<MX_FORMAT_E2M1>(a, gated, stream);
+    gated ? launch_rows<MX_FORMAT_E2M1, true>(a, stream) : launch_rows<MX_FORMAT_E2M1, false>(a, stream);
   else
-    launch_rows<MX_FORMAT_E4M3>(a, gated, stream);
+    gated ? launch_rows<MX_FORMAT_E4M3, true>(a, stream) : launch_rows<MX_FORMAT_E4M3, false>(a, stream);
   return hipGetLastError();
 }
 

@@ -12,6 +12,7 @@ constexpr int64_t kMaxLd = (int64_t)1 << 31;
 constexpr int64_t kMaxK = (int64_t)1 << 23;             // a tile's row offsets are 32 bits
 constexpr int64_t kMaxWeights = (int64_t)1 << 36;       // a group's scale offsets are 32 bits
 constexpr int64_t kMaxCols = (int64_t)1 << 24;          // and those of 32 rows of a result
+constexpr int64_t kMaxDecodeLd = (int64_t)1 << 24;     // and those of a few rows of x
 constexpr int64_t kMaxCast = (int64_t)1 << 35;
 
 bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p % a) == 0; }
@@ -61,7 +62,7 @@ mx_status decode(const void* x, int64_t ldx, const uint8_t* qw, const uint8_t* s
                  int64_t n, int64_t w_rows, int64_t k, bool gated, bool gelu, void* c, int32_t c_type,
                  hipStream_t stream) {
   if (!product_ok(m, w_rows, k, 0) || m > MX_MAX_DECODE_ROWS || !format_ok(w_format) || !type_ok(c_type) || ldx < k ||
-      ldx > kMaxLd)
+      ldx > kMaxDecodeLd)
     return MX_ERR_SHAPE;
   if (m == 0 || n == 0)
     return MX_OK;
