@@ -23,18 +23,20 @@ struct Cast4Args {
   uint32_t row_tiles, col_tiles;   // of a matrix
 };
 
-// Eight consecutive elements of a row as loaded, from any element on.
-template <typename T>
-struct Eight {
-  static constexpr int kWords = 8 * (int)sizeof(T) / 16;
+// N consecutive elements of a row as loaded, from any element on.
+template <typename T, int N = 8>
+struct Run {
+  static constexpr int kWords = N * (int)sizeof(T) / 16;
   u32x4 w[kWords];
+  // (streaming: 8192 x 5120 binary32 in both directions 47.8 -> 40.8 us, 16640 x
+  // 5120 bf16 along rows 38.5 -> 36.8; along rows of binary32 66.6 -> 68.7)
+  template <bool STREAM>
   __device__ __forceinline__ void load(const T* p) {
-    struct __attribute__((packed, aligned(sizeof(T)))) Word {
-      u32x4 v;
-    };
+    typedef u32x4 Word __attribute__((aligned(2)));   // (of binary32 4)
 #pragma unroll
     for (int i = 0; i < kWords; ++i)
-      w[i] = reinterpret_cast<const Word*>(p)[i].v;
+      w[i] = STREAM ? __builtin_nontemporal_load(reinterpret_cast<const Word*>(p) + i)
+                    : reinterpret_cast<const Word*>(p)[i];
   }
   __device__ __forceinline__ void clear() {
 #pragma unroll
@@ -52,7 +54,7 @@ struct Eight {
     if constexpr (sizeof(T) == 4) {
       uint32_t m = 0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
+      for (int i = 0; i < N; ++i)
         m = max(m, w[i / 4][i % 4] & 0x7FFFFFFFu);
       return m;
     } else {
@@ -80,15 +82,18 @@ template <int SEL>
 __device__ __forceinline__ uint32_t pair4(uint32_t old, uint32_t bf16s, float scale) {
   return __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(old, __builtin_bit_cast(bf16x2, bf16s), scale, SEL);
 }
-template <typename T>
-__device__ __forceinline__ uint32_t codes8(const Eight<T>& d, uint32_t byte) {
+// N codes, the first in the lowest bits.
+template <typename T, int N>
+__device__ __forceinline__ uint32_t codes(const Run<T, N>& d, uint32_t byte) {
   const float scale = __uint_as_float(byte << 23);
   uint32_t q = 0;
   if constexpr (sizeof(T) == 4) {
     q = pair4<0>(q, d.get(0), d.get(1), scale);
     q = pair4<1>(q, d.get(2), d.get(3), scale);
-    q = pair4<2>(q, d.get(4), d.get(5), scale);
-    q = pair4<3>(q, d.get(6), d.get(7), scale);
+    if constexpr (N == 8) {
+      q = pair4<2>(q, d.get(4), d.get(5), scale);
+      q = pair4<3>(q, d.get(6), d.get(7), scale);
+    }
   } else {
     q = pair4<0>(q, d.w[0][0], scale);
     q = pair4<1>(q, d.w[0][1], scale);
@@ -106,78 +111,115 @@ __device__ __forceinline__ int64_t blocked_at(int64_t r, int64_t c, int64_t stri
 
 constexpr int kCast4Threads = 256;
 
-// dim0 alone: a lane owns eight columns of a row, a quad a block.  Blocked
-// scales: the lanes also cover the layout's padding, whose bytes they clear.
+// dim0 alone: a lane owns eight columns of a row, a quad a block.  Of bf16 a lane
+// has two of those, whose loads are on their way together (16640 x 5120: 44.0 ->
+// 36.8 us, 5.9 TB/s); of binary32, 32 bytes each, one (66.6 us, 5.8 TB/s; two
+// 69.7).  Blocked scales: the lanes also cover the layout's padding, whose bytes
+// they clear.
+template <typename T>
+constexpr int kCast4Runs = sizeof(T) == 2 ? 2 : 1;
 template <typename T>
 __global__ __launch_bounds__(kCast4Threads) void cast4_rows_kernel(Cast4Args a) {
-  const int64_t blocks = a.cols / 32;
-  const int64_t pblocks = a.blocked ? (blocks + 3) / 4 * 4 : blocks;
-  const int64_t prows = a.blocked ? (a.rows + 127) / 128 * 128 : a.rows;
-  const int64_t unit = (int64_t)blockIdx.x * kCast4Threads + threadIdx.x, units = pblocks * 4;
-  const int64_t row = unit / units;                 // of all matrices
-  if (row >= a.batch * prows)
-    return;   // whole quads: units is a multiple of 4
-  const int64_t b = row / prows, r = row % prows, c = (unit - row * units) * 8;
-  const bool on = r < a.rows && c < a.cols;
-  Eight<T> d;
-  d.clear();
-  if (on)
-    d.load(static_cast<const T*>(a.x) + (b * a.rows + r) * a.ldx + c);
-  uint32_t m = d.amax();
-  m = max(m, quad_swap1(m));
-  m = max(m, quad_swap2(m));
-  const uint32_t byte = on ? scale4(m) : 0;
-  if (on)
-    *reinterpret_cast<uint32_t*>(a.q0 + ((b * a.rows + r) * a.cols + c) / 2) = codes8(d, byte);
-  if ((threadIdx.x & 3) == 0) {
-    const int64_t at = a.blocked ? b * prows * pblocks + blocked_at(r, c / 32, pblocks * 128) : row * blocks + c / 32;
-    a.s0[at] = (uint8_t)byte;
+  const uint32_t blocks = (uint32_t)(a.cols / 32), pblocks = a.blocked ? (blocks + 3) / 4 * 4 : blocks;
+  const uint32_t prows = (uint32_t)(a.blocked ? (a.rows + 127) / 128 * 128 : a.rows), units = pblocks * 4;
+  const uint32_t all = (uint32_t)a.batch * prows;
+  constexpr int kRuns = kCast4Runs<T>;
+  Run<T> d[kRuns];
+  uint32_t row[kRuns], r[kRuns], c[kRuns];
+  bool on[kRuns];
+#pragma unroll
+  for (int i = 0; i < kRuns; ++i) {
+    const uint32_t unit = (blockIdx.x * kRuns + i) * kCast4Threads + threadIdx.x;
+    row[i] = unit / units;   // of all matrices; whole quads (units is a multiple of 4)
+    c[i] = (unit - row[i] * units) * 8;
+    r[i] = row[i] % prows;
+    on[i] = row[i] < all && r[i] < a.rows && c[i] < a.cols;
+    d[i].clear();
+    if (on[i])
+      d[i].template load<sizeof(T) == 2>(static_cast<const T*>(a.x) + ((int64_t)(row[i] / prows) * a.rows + r[i]) * a.ldx + c[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < kRuns; ++i) {
+    const int64_t b = row[i] / prows;
+    uint32_t m = d[i].amax();
+    m = max(m, quad_swap1(m));
+    m = max(m, quad_swap2(m));
+    const uint32_t byte = on[i] ? scale4(m) : 0;
+    if (on[i])
+      *reinterpret_cast<uint32_t*>(a.q0 + ((b * a.rows + r[i]) * a.cols + c[i]) / 2) = codes(d[i], byte);
+    if ((threadIdx.x & 3) == 0 && row[i] < all) {
+      const int64_t at = a.blocked ? b * prows * pblocks + blocked_at(r[i], c[i] / 32, (int64_t)pblocks * 128)
+                                   : (int64_t)row[i] * blocks + c[i] / 32;
+      a.s0[at] = (uint8_t)byte;
+    }
   }
 }
 
-// Both directions, or dim1 alone: a workgroup of eight waves owns 256 x 256
-// elements, a wave 32 rows of them, a lane 16 rows of eight columns, so that a
-// block along the rows is a quad's and one along the columns two lanes'.
-// Column codes and all scales leave through LDS: 128 bytes of a column's codes
-// and four scales (a word of the blocked layout) at a time.
-constexpr int kCast4Tile = 256;
-constexpr int kCast4Pitch = kCast4Tile / 2 + 16;
+// Both directions, or dim1 alone: a workgroup of four waves owns 128 rows of 32 C
+// columns, a wave 32 rows of them, a lane 16 rows of C columns, 16 bytes each,
+// so that a block along the rows is 32 / C lanes' and one along the columns two
+// lanes'.  Column codes and all scales leave through LDS: 64 bytes of a column's
+// codes and four scales (a word of the blocked layout) at a time.  16640 x 5120
+// bf16 61 us (4.3 TB/s), 8192 x 5120 binary32 41 (5.2 TB/s; eight columns to a
+// lane took 158 registers, one workgroup to a CU: 62).  Eight waves and 128 bytes
+// a column are even there and slower on small matrices (2048 x 2048 8.9 -> 9.9
+// us); tiles in pieces per XCD, along rows or columns, gained nothing.
+constexpr int kCast4Waves = 4, kCast4Rows = 32 * kCast4Waves;
+constexpr int kCast4Pitch = kCast4Rows / 2 + 16;
+template <typename T>
+constexpr int kCast4Cols = 32 * 16 / (int)sizeof(T);
 
 template <typename T>
-__global__ __launch_bounds__(512) void cast4_both_kernel(Cast4Args a) {
-  __shared__ __attribute__((aligned(16))) uint8_t qt[kCast4Tile * kCast4Pitch];
-  __shared__ __attribute__((aligned(16))) uint8_t st[2][kCast4Tile][8];   // scales along dim0 by row, dim1 by column
+__global__ __launch_bounds__(64 * kCast4Waves) void cast4_both_kernel(Cast4Args a) {
+  constexpr int C = 16 / (int)sizeof(T), kCols = 32 * C;
+  __shared__ __attribute__((aligned(16))) uint8_t qt[kCols * kCast4Pitch];
+  __shared__ __attribute__((aligned(16))) uint8_t sr[kCast4Rows][kCols / 32], sc[kCols][kCast4Rows / 32];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const uint32_t tiles = a.row_tiles * a.col_tiles;
   const int64_t b = blockIdx.x / tiles;
   const uint32_t tile = blockIdx.x % tiles;
-  const int64_t row0 = (int64_t)(tile / a.col_tiles) * kCast4Tile, col0 = (int64_t)(tile % a.col_tiles) * kCast4Tile;
-  const int lr = 32 * wave + 16 * (lane >> 5), lc = 8 * (lane & 31);
+  const int64_t row0 = (int64_t)(tile / a.col_tiles) * kCast4Rows, col0 = (int64_t)(tile % a.col_tiles) * kCols;
+  const int lr = 32 * wave + 16 * (lane >> 5), lc = C * (lane & 31);
   const bool on = row0 + lr < a.rows && col0 + lc < a.cols;
   const T* x = static_cast<const T*>(a.x) + (b * a.rows + row0 + lr) * a.ldx + col0 + lc;
-  Eight<T> d[16];
+  Run<T, C> d[16];
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
     d[i].clear();
     if (on)
-      d[i].load(x + i * a.ldx);
+      d[i].template load<true>(x + i * a.ldx);
   }
   if (a.q0 != nullptr) {
     uint8_t* q0 = a.q0 + ((b * a.rows + row0 + lr) * a.cols + col0 + lc) / 2;
+    uint32_t before = 0;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       uint32_t m = d[i].amax();
       m = max(m, quad_swap1(m));
       m = max(m, quad_swap2(m));
-      const uint32_t byte = on ? scale4(m) : 0;
-      if (on)
-        *reinterpret_cast<uint32_t*>(q0 + i * (a.cols / 2)) = codes8(d[i], byte);
-      if ((lane & 3) == 0)
-        st[0][lr + i][(lane & 31) / 4] = (uint8_t)byte;
+      if constexpr (C == 4)
+        m = max(m, half_row_mirror(m));
+      const uint32_t byte = on ? scale4(m) : 0, q = codes(d[i], byte);
+      if constexpr (C == 8) {
+        if (on)
+          *reinterpret_cast<uint32_t*>(q0 + i * (a.cols / 2)) = q;
+      } else if (i % 2 == 0) {
+        before = q;
+      } else {
+        // two rows' 2 bytes of two lanes: the even lane stores the first row's
+        // 4 bytes, the odd lane the second's
+        const bool odd = lane & 1;
+        const uint32_t other = quad_swap1(odd ? before : q);
+        if (on)
+          *reinterpret_cast<uint32_t*>(q0 + (odd ? i * (a.cols / 2) - 2 : (i - 1) * (a.cols / 2))) =
+              odd ? other | (q << 16) : before | (other << 16);
+      }
+      if ((lane & (32 / C - 1)) == 0)
+        sr[lr + i][(lane & 31) * C / 32] = (uint8_t)byte;
     }
   }
 #pragma unroll
-  for (int c = 0; c < 8; ++c) {
+  for (int c = 0; c < C; ++c) {
     uint32_t m = 0;
 #pragma unroll
     for (int i = 0; i < 16; ++i)
@@ -197,22 +239,20 @@ __global__ __launch_bounds__(512) void cast4_both_kernel(Cast4Args a) {
       q = (u32x2){0, 0};
     *reinterpret_cast<u32x2*>(qt + (lc + c) * kCast4Pitch + lr / 2) = q;
     if (lane < 32)
-      st[1][lc + c][wave] = (uint8_t)byte;
+      sc[lc + c][wave] = (uint8_t)byte;
   }
   __syncthreads();
   // rows are multiples of 32: a word holds whole blocks
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int c = 64 * i + threadIdx.x / 8, byte = 16 * (threadIdx.x % 8);
+  for (int i = 0; i < kCols / 64; ++i) {   // 16 bytes a thread, kCast4Waves of them a column
+    const int c = 64 * i + threadIdx.x / kCast4Waves, byte = 16 * (threadIdx.x % kCast4Waves);
     if (col0 + c < a.cols && row0 + 2 * byte < a.rows)
       *reinterpret_cast<u32x4*>(a.q1 + ((b * a.cols + col0 + c) * a.rows + row0) / 2 + byte) =
           *reinterpret_cast<const u32x4*>(qt + c * kCast4Pitch + byte);
   }
-  // four scales a thread: line l (a row, or a column) of the tile, blocks 4 h on
-  auto scales = [&](uint8_t* s, int which, int64_t line0, int64_t lines, int64_t block0, int64_t blocks) {
-    const int l = threadIdx.x >> 1, h = threadIdx.x & 1;
-    const int64_t line = line0 + l, first = block0 + 4 * h;
-    const uint32_t word = *reinterpret_cast<const uint32_t*>(&st[which][l][4 * h]);
+  // four scales a thread: blocks `first` on of a line (a row, or a column)
+  auto scales = [&](uint8_t* s, const uint8_t* from, int64_t line, int64_t lines, int64_t first, int64_t blocks) {
+    const uint32_t word = *reinterpret_cast<const uint32_t*>(from);
     if (a.blocked) {
       const int64_t pl = (lines + 127) / 128 * 128, pb = (blocks + 3) / 4 * 4;
       if (line < pl && first < pb)
@@ -224,38 +264,44 @@ __global__ __launch_bounds__(512) void cast4_both_kernel(Cast4Args a) {
           s[(b * lines + line) * blocks + first + i] = (uint8_t)(word >> (8 * i));
     }
   };
+  constexpr int kRowWords = kCols / 128, kColWords = kCast4Waves / 4;   // words of a line's scales
   if (a.q0 != nullptr)
-    scales(a.s0, 0, row0, a.rows, col0 / 32, a.cols / 32);
-  scales(a.s1, 1, col0, a.cols, row0 / 32, a.rows / 32);
+    for (int t = threadIdx.x; t < kCast4Rows * kRowWords; t += 64 * kCast4Waves)
+      scales(a.s0, &sr[t / kRowWords][4 * (t % kRowWords)], row0 + t / kRowWords, a.rows,
+             col0 / 32 + 4 * (t % kRowWords), a.cols / 32);
+  for (int t = threadIdx.x; t < kCols * kColWords; t += 64 * kCast4Waves)
+    scales(a.s1, &sc[t / kColWords][4 * (t % kColWords)], col0 + t / kColWords, a.cols,
+           row0 / 32 + 4 * (t % kColWords), a.rows / 32);
 }
 
-static Cast4Args cast4_args(int64_t batch, int64_t rows, int64_t cols) {
+static Cast4Args cast4_args(int64_t batch, int64_t rows, int64_t cols, int tile_cols) {
   Cast4Args a = {};
   a.batch = batch, a.rows = rows, a.cols = cols;
-  a.row_tiles = (uint32_t)((rows + kCast4Tile - 1) / kCast4Tile);
-  a.col_tiles = (uint32_t)((cols + kCast4Tile - 1) / kCast4Tile);
+  a.row_tiles = (uint32_t)((rows + kCast4Rows - 1) / kCast4Rows);
+  a.col_tiles = (uint32_t)((cols + tile_cols - 1) / tile_cols);
   return a;
 }
 
-static int64_t rows_blocks(int64_t batch, int64_t rows, int64_t cols, bool blocked) {
+static int64_t rows_blocks(int64_t batch, int64_t rows, int64_t cols, bool blocked, int runs) {
   const int64_t b = cols / 32, pb = blocked ? (b + 3) / 4 * 4 : b, pr = blocked ? (rows + 127) / 128 * 128 : rows;
-  return (batch * pr * pb * 4 + kCast4Threads - 1) / kCast4Threads;
+  return (batch * pr * pb * 4 + kCast4Threads * runs - 1) / (kCast4Threads * runs);
 }
 
-int64_t cast4_grid_blocks(int64_t batch, int64_t rows, int64_t cols) { return rows_blocks(batch, rows, cols, true); }
+int64_t cast4_grid_blocks(int64_t batch, int64_t rows, int64_t cols) { return rows_blocks(batch, rows, cols, true, 1); }
 
 hipError_t launch_cast4(const void* x, int64_t batch, int64_t rows, int64_t cols, int64_t ldx, bool f32, uint8_t* q0,
                         uint8_t* s0, uint8_t* q1, uint8_t* s1, bool blocked, hipStream_t stream) {
-  Cast4Args a = cast4_args(batch, rows, cols);
+  Cast4Args a = cast4_args(batch, rows, cols, f32 ? kCast4Cols<float> : kCast4Cols<uint16_t>);
   a.x = x, a.ldx = ldx, a.q0 = q0, a.s0 = s0, a.q1 = q1, a.s1 = s1, a.blocked = blocked;
   if (q1 == nullptr) {
-    const dim3 grid((unsigned)rows_blocks(batch, rows, cols, blocked)), threads(kCast4Threads);
+    const int runs = f32 ? kCast4Runs<float> : kCast4Runs<uint16_t>;
+    const dim3 grid((unsigned)rows_blocks(batch, rows, cols, blocked, runs)), threads(kCast4Threads);
     if (f32)
       hipLaunchKernelGGL(cast4_rows_kernel<float>, grid, threads, 0, stream, a);
     else
       hipLaunchKernelGGL(cast4_rows_kernel<uint16_t>, grid, threads, 0, stream, a);
   } else {
-    const dim3 grid((unsigned)(batch * a.row_tiles * a.col_tiles)), threads(512);
+    const dim3 grid((unsigned)(batch * a.row_tiles * a.col_tiles)), threads(64 * kCast4Waves);
     if (f32)
       hipLaunchKernelGGL(cast4_both_kernel<float>, grid, threads, 0, stream, a);
     else

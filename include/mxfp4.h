@@ -52,7 +52,7 @@ extern "C" {
  * Either output pair may be NULL (both members); both pairs NULL, a half-NULL
  * pair or x NULL -> MX_ERR_NULL.  cols a multiple of 32; rows any, but a
  * multiple of 32 where q_col is given; cols <= ldx <= 2^31; batch * (rows
- * rounded up to 128) * (cols rounded up to 128) < 2^35; else MX_ERR_SHAPE.
+ * rounded up to 128) * (cols rounded up to 128) < 2^34; else MX_ERR_SHAPE.
  */
 MX_API mx_status mx_cast_mxfp4(const void* x, int32_t x_type, int64_t batch, int64_t rows, int64_t cols, int64_t ldx,
                                uint8_t* q_row, uint8_t* s_row, uint8_t* q_col, uint8_t* s_col, int32_t blocked,
