@@ -443,7 +443,10 @@ inline MmArgs mm_args(const MmOperands& in, int64_t m, int64_t n, int64_t w_rows
 }
 
 // Whether a result of m rows and n columns is taken in large tiles: where they
-// fill the GPU.  tile_cols: columns of R that a large tile covers.
+// nearly fill the GPU.  tile_cols: columns of R that a large tile covers.
+// (Timed, large against small: 256 tiles, 4096 x 4096 x 4096 with MXFP8 rows 52
+// us against 60; 128 tiles, 4096 x 2048 x 2048 25 against 18; 64 tiles, 2048 x
+// 2048 x 4096 in 4 bits 27 against 14.)
 inline bool mm_large(int64_t m, int64_t n, int32_t groups, int tile_cols) {
   const int64_t rows = groups > 1 ? m / groups : m;   // (of a group, if they were even)
   const int64_t tiles = (rows + 255) / 256 * (groups > 1 ? groups : 1) * ((n + tile_cols - 1) / tile_cols);
