@@ -109,8 +109,11 @@ __global__ __launch_bounds__(64 * KS) void decode_kernel(DecodeArgs a) {
 #pragma unroll
     for (int t = 0; t < TB; ++t)
       acc[i][t] = (f32x4){};
-  auto multiply = [&](int b) {
+  const int blocks = (int)(a.k / 32);
+  auto multiply = [&](int ch, int b) {
     const uint8_t* at = lds + (wave * BUFS + b) * B::kBytes;
+    // (scale 0 past K: the layout's padding may hold anything, a NaN too)
+    const uint32_t keep = 4 * ch + q < blocks ? 0xFFu : 0u;
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
       u32x4 w[kWords];
@@ -118,7 +121,7 @@ __global__ __launch_bounds__(64 * KS) void decode_kernel(DecodeArgs a) {
       for (int v = 0; v < kWords; ++v)
         w[v] = *reinterpret_cast<const u32x4*>(at + B::kW + (16 * i + c) * B::kRow +
                                                16 * ((kWords * q + v) ^ mm_swizzle<kPieces>(c)));
-      const uint32_t byte = at[B::kS + 4 * (16 * i + c) + q];
+      const uint32_t byte = at[B::kS + 4 * (16 * i + c) + q] & keep;
       const float scale = __uint_as_float(byte << 23);
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
@@ -159,7 +162,7 @@ __global__ __launch_bounds__(64 * KS) void decode_kernel(DecodeArgs a) {
     load(ch + KS * (BUFS - 1), b == 0 ? BUFS - 1 : b - 1);
     mm_wait_loads<(BUFS - 1) * B::kLoads>();
     mm_wave_fence();
-    multiply(b);
+    multiply(ch, b);
     mm_wave_fence();
     __builtin_amdgcn_s_waitcnt(0xC07F);   // its reads are done (lgkmcnt 0) before the buffer is loaded again
     b = b + 1 == BUFS ? 0 : b + 1;

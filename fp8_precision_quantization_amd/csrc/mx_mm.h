@@ -344,7 +344,7 @@ __device__ __forceinline__ void mm_tile(const MmArgs& a, const MmPlace& p, int64
     else
       return (v8i){(int)o[0][0], (int)o[0][1], (int)o[0][2], (int)o[0][3], 0, 0, 0, 0};
   };
-  // MFMA q of step s: scale byte 2 s + h of a row's word, h shifted away before
+  // MFMA q of step s: scale byte 2 s + h of a row's word, taken from 2 s on
   constexpr int kMfmas = BX * BW;
   auto mfma = [&](auto s_c, int q, const OpX& ox, const OpW& ow) {
     constexpr int kByte = 2 * decltype(s_c)::value;
@@ -388,14 +388,18 @@ __device__ __forceinline__ void mm_tile(const MmArgs& a, const MmPlace& p, int64
   using S0 = std::integral_constant<int, 0>;
   using S1 = std::integral_constant<int, 1>;
   auto reads_by = [](int q) { return min(q * 2 * kReads / kMfmas, kReads); };
+  // A row's scales of a stage: bytes h and h + 2 of a word to bits 0 and 16, and
+  // 0 for blocks past K (the layout's padding may hold anything, a NaN too).
+  const int tail = min(24, 8 * ((int)(a.k / 32) - 4 * (stages - 1) - h));
   int b = 0;
   for (int t = 0; t < stages; ++t) {
+    const uint32_t bits = t == stages - 1 ? tail : 24;
 #pragma unroll
     for (int i = 0; i < BW; ++i)
-      sw[i] = nw[i] >> (8 * h);
+      sw[i] = __builtin_amdgcn_ubfe(nw[i], 8 * h, bits);
 #pragma unroll
     for (int j = 0; j < BX; ++j)
-      sx[j] = nx[j] >> (8 * h);
+      sx[j] = __builtin_amdgcn_ubfe(nx[j], 8 * h, bits);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int q = 0; q < kMfmas; ++q) {

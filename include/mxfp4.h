@@ -8,7 +8,8 @@
  * caller-owned buffers and stream, no allocation, no synchronisation, no host
  * read of device memory, host validation before any HIP call, asynchronous;
  * outputs must not overlap inputs or each other; the same bits in every call on
- * the same inputs; binary32 sums, one rounding of a bf16 result at the end.
+ * the same inputs; binary32 sums, one rounding of a bf16 result at the end;
+ * padding bytes of a blocked scale layout that is read may hold anything.
  *
  * MXFP4 rule:
  *   amax  = max |x| over a block of 32 (NaN > +Inf > finite);

@@ -43,7 +43,8 @@ def test_cast_validation(lib):
         return lib.mx_cast_mxfp4(x, t, batch, rows, cols, ldx, q0, s0, q1, s1, blocked, None)
     for bad in (dict(t=2), dict(batch=-1), dict(rows=-32), dict(cols=-32), dict(cols=48, ldx=48), dict(ldx=63),
                 dict(rows=33), dict(ldx=(1 << 31) + 1), dict(rows=HUGE), dict(batch=HUGE), dict(cols=HUGE, ldx=HUGE),
-                dict(batch=1 << 21, rows=128, cols=128, ldx=128), dict(batch=1, rows=1 << 28, cols=128, ldx=128)):
+                dict(batch=1 << 21, rows=128, cols=128, ldx=128), dict(batch=1, rows=1 << 28, cols=128, ldx=128),
+                dict(batch=1 << 20, rows=97, cols=128, ldx=128, q1=None, s1=None)):
         assert f(**bad) == SHAPE, bad
     for bad in (dict(x=None), dict(q0=None), dict(s0=None), dict(q1=None), dict(s1=None),
                 dict(q0=None, s0=None, q1=None, s1=None)):
@@ -69,7 +70,7 @@ def test_gemm_validation(lib):
         return lib.mx_grouped_gemm_mxfp4(qa, sa, fa, qb, sb, ends, groups, m, n, k, c, t, None)
     for call in (f, g):
         for bad in (dict(fa=2), dict(fa=-1), dict(t=2), dict(m=-1), dict(n=-1), dict(k=-32), dict(k=48),
-                    dict(k=(1 << 23) + 32), dict(n=1 << 14, k=1 << 22), dict(m=(1 << 31) - 1), dict(n=1 << 31),
+                    dict(k=(1 << 23) + 32), dict(n=1 << 14, k=1 << 22), dict(m=(1 << 31) - 1), dict(n=(1 << 24) + 1), dict(n=1 << 31),
                     dict(m=1 << 30, n=1 << 30), dict(m=1 << 30, n=1 << 30, k=32), dict(m=HUGE), dict(n=HUGE), dict(k=HUGE)):
             assert call(**bad) == SHAPE, bad
         for bad in (dict(qa=None), dict(sa=None), dict(qb=None), dict(sb=None), dict(c=None)):
@@ -89,7 +90,7 @@ def test_decode_validation(lib):
         return lib.mx_gated_ffn_decode(x, ldx, qw, sw, fw, m, n, k, act, c, None)
     for call in (f, g):
         for bad in (dict(fw=2), dict(m=-1), dict(m=65), dict(n=-1), dict(k=-32), dict(k=40), dict(ldx=63),
-                    dict(ldx=BIG), dict(k=(1 << 23) + 32, ldx=1 << 24), dict(n=1 << 31), dict(n=HUGE),
+                    dict(ldx=BIG), dict(ldx=(1 << 24) + 1), dict(k=(1 << 23) + 32, ldx=1 << 24), dict(n=1 << 31), dict(n=HUGE),
                     dict(n=1 << 14, k=1 << 22, ldx=1 << 22)):
             assert call(**bad) == SHAPE, bad
         for bad in (dict(x=None), dict(qw=None), dict(sw=None), dict(c=None)):
@@ -108,7 +109,7 @@ def test_ffn_validation(lib):
         return lib.mx_gated_ffn_backward(qx, sx, fx, qw, sw, fw, ends, groups, rows, cols, k, act, q, s, dh, y, None)
     for call in (f, g):
         for bad in (dict(fx=2), dict(fw=-1), dict(fx=1, fw=0), dict(act=2), dict(rows=-1), dict(cols=-32), dict(cols=48),
-                    dict(k=40), dict(k=-32), dict(k=(1 << 23) + 32), dict(rows=(1 << 31) - 1), dict(cols=1 << 31),
+                    dict(k=40), dict(k=-32), dict(k=(1 << 23) + 32), dict(rows=(1 << 31) - 1), dict(cols=1 << 31), dict(cols=(1 << 24) + 32),
                     dict(cols=HUGE), dict(rows=HUGE), dict(k=HUGE), dict(cols=1 << 14, k=1 << 22),
                     dict(rows=1 << 30, cols=1 << 24, k=32)):
             assert call(**bad) == SHAPE, bad
