@@ -65,12 +65,16 @@ __global__ __launch_bounds__(64 * KS) void decode_kernel(DecodeArgs a) {
   const int ldw = (int)(kFp4 ? a.k / 2 : a.k), strip = (int)((a.k / 32 + 3) / 4) * 512;
   const int chunks = (int)((a.k + 127) / 128);
 
-  // Ranges over the workgroup's rows of each half of W and all of x: rows past
-  // the end, and K past it (an offset outside), read as zeros.
+  // Ranges over the workgroup's rows of each half of W, and four rows of x at a
+  // time (which may lie far apart): rows past the end, and K past it (an offset
+  // outside), read as zeros.
   const int64_t rows = min((int64_t)16 * RB, a.n - j0), up = GATED ? a.n : 0;
   const __amdgpu_buffer_rsrc_t rw = buffer_rsrc(a.qw + j0 * ldw, (uint32_t)(rows * ldw));
   const __amdgpu_buffer_rsrc_t ru = GATED ? buffer_rsrc(a.qw + (j0 + up) * ldw, (uint32_t)(rows * ldw)) : rw;
-  const __amdgpu_buffer_rsrc_t rx = buffer_rsrc(a.x, (uint32_t)(((a.m - 1) * a.ldx + a.k) * 2));
+  auto four_rows = [&](int u) {
+    const int rows = min(4, a.m - 4 * u);
+    return buffer_rsrc(a.x + (rows > 0 ? 4 * u * a.ldx : 0), rows > 0 ? (uint32_t)(((rows - 1) * a.ldx + a.k) * 2) : 0u);
+  };
   // scale words: lane l's is of W's row l of the workgroup's, gate's rows first
   const int64_t srow0 = j0 / 128 * 128, srows = (a.n + up + 127) / 128 * 128 - srow0;
   const __amdgpu_buffer_rsrc_t rs = buffer_rsrc(a.sw + srow0 / 128 * strip, (uint32_t)(srows / 128 * strip));
@@ -89,9 +93,8 @@ __global__ __launch_bounds__(64 * KS) void decode_kernel(DecodeArgs a) {
     const uint32_t to = mine + b * B::kBytes;
 #pragma unroll
     for (int u = 0; u < TB * 4; ++u) {
-      const int row = 4 * u + xrow, k = 128 * ch + 8 * ((lane % 16) ^ (row % 16));
-      mm_load<16>(to + B::kX + u * 1024, rx,
-                  row < a.m && k < a.k ? ((uint32_t)row * (uint32_t)a.ldx + k) * 2 : 0x80000000u);
+      const int k = 128 * ch + 8 * ((lane % 16) ^ ((4 * u + xrow) % 16));
+      mm_load<16>(to + B::kX + u * 1024, four_rows(u), k < a.k ? ((uint32_t)xrow * (uint32_t)a.ldx + k) * 2 : 0x80000000u);
     }
 #pragma unroll
     for (int u = 0; u < B::kLoadsW; ++u) {

@@ -12,7 +12,7 @@ constexpr int64_t kMaxLd = (int64_t)1 << 31;
 constexpr int64_t kMaxK = (int64_t)1 << 23;             // a tile's row offsets are 32 bits
 constexpr int64_t kMaxWeights = (int64_t)1 << 36;       // a group's scale offsets are 32 bits
 constexpr int64_t kMaxCols = (int64_t)1 << 24;          // and those of 32 rows of a result
-constexpr int64_t kMaxDecodeLd = (int64_t)1 << 24;     // and those of a few rows of x
+constexpr int64_t kMaxDecodeLd = (int64_t)1 << 28;      // and those of four rows of x
 constexpr int64_t kMaxCast = (int64_t)1 << 34;
 
 bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p % a) == 0; }

@@ -105,7 +105,7 @@ MX_API mx_status mx_grouped_gemm_mxfp4(const uint8_t* qa, const uint8_t* sa, int
  * x enters as it is; a code times its scale is exact in bf16 but for e4m3
  * values under scale bytes 0 to 2 (rounded to a multiple of 2^-133).
  * 0 <= m <= MX_MAX_DECODE_ROWS, n < 2^31, k % 32 == 0, 0 <= k <= 2^23, n * k <
- * 2^36, k <= ldx <= 2^24, else MX_ERR_SHAPE; m or n 0 writes nothing; k 0
+ * 2^36, k <= ldx <= 2^28, else MX_ERR_SHAPE; m or n 0 writes nothing; k 0
  * writes zeros.
  */
 MX_API mx_status mx_linear_decode(const void* x, int64_t ldx, const uint8_t* qw, const uint8_t* sw, int32_t w_format,

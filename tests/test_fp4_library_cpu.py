@@ -90,7 +90,7 @@ def test_decode_validation(lib):
         return lib.mx_gated_ffn_decode(x, ldx, qw, sw, fw, m, n, k, act, c, None)
     for call in (f, g):
         for bad in (dict(fw=2), dict(m=-1), dict(m=65), dict(n=-1), dict(k=-32), dict(k=40), dict(ldx=63),
-                    dict(ldx=BIG), dict(ldx=(1 << 24) + 1), dict(k=(1 << 23) + 32, ldx=1 << 24), dict(n=1 << 31), dict(n=HUGE),
+                    dict(ldx=BIG), dict(ldx=(1 << 28) + 1), dict(k=(1 << 23) + 32, ldx=1 << 24), dict(n=1 << 31), dict(n=HUGE),
                     dict(n=1 << 14, k=1 << 22, ldx=1 << 22)):
             assert call(**bad) == SHAPE, bad
         for bad in (dict(x=None), dict(qw=None), dict(sw=None), dict(c=None)):

@@ -87,6 +87,21 @@ def test_rows_at_any_pitch_and_start(pad, first, oracle_mod):
     assert torch.equal(y, mx.mx_linear_decode(x.contiguous(), qw, sw, out_dtype=torch.float32))
 
 
+@pytest.mark.parametrize("m,pitch", [(5, (1 << 25) + 32), (2, 1 << 28)])
+def test_last_tokens_of_long_sequences(m, pitch, oracle_mod):
+    """Rows of x far apart, as the last tokens of (batch, tokens, K) lie."""
+    dev = device()
+    rng = np.random.default_rng(m)
+    n, k = 40, 160
+    qw, sw, w = _weights(oracle_mod, rng, n, k, "e2m1", dev)
+    v, x = _x(rng, m, k, dev)
+    wide = torch.full(((m - 1) * pitch + k,), float("nan"), dtype=torch.bfloat16, device=dev)
+    far = wide.as_strided((m, k), (pitch, 1))
+    far.copy_(x)
+    assert torch.equal(mx.mx_linear_decode(far, qw, sw), mx.mx_linear_decode(x, qw, sw))
+    assert torch.equal(mx.mx_gated_ffn_decode(far, qw, sw), mx.mx_gated_ffn_decode(x, qw, sw))
+
+
 def test_nan_blocks_and_infinite_x(oracle_mod):
     """A block of scale 0xFF makes its column NaN; Inf and NaN of x stay in
     their row; the other rows and columns do not see them."""
