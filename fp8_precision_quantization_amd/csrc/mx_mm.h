@@ -142,7 +142,7 @@ struct MmPlace {
 // left open).  XCD x (workgroups are dealt to the XCDs in turn) owns one of 8
 // contiguous pieces of the ordered tiles: bands of 8 tile rows, column by
 // column.  Grouped: a piece of each group's tiles, group after group.  `lds`
-// holds the group table meanwhile.
+// holds the table of many groups meanwhile.
 template <bool GROUPED, int TILE>
 __device__ __forceinline__ bool mm_place(const MmArgs& a, uint8_t* lds, MmPlace& p) {
   auto band_tile = [&](uint32_t i, uint32_t rows_of_tiles, uint32_t& tm) {
@@ -164,17 +164,52 @@ __device__ __forceinline__ bool mm_place(const MmArgs& a, uint8_t* lds, MmPlace&
     p.srow0 = p.row0;
     return true;
   } else {
+    const int32_t q = (int32_t)(blockIdx.x / 8), x = (int32_t)(blockIdx.x % 8);
+    // A few groups: every wave finds its tile by itself in a uniform loop, the
+    // ends eight at a time (past the last they repeat it: no rows).
+    if (a.groups <= kScalarTableGroups) {
+      int32_t run = 0, lo = 0, hi = 0, first = 0, part = 0;   // first: the group's first of each XCD's workgroups
+      uint32_t trows = 0, pg = 0;
+      int g = -1;
+      // (constant memory to the kernel: scalar loads)
+      const auto* all = (const __attribute__((address_space(4))) int32_t*)(uintptr_t)a.ends;
+      for (int g0 = 0; g0 < a.groups && g < 0; g0 += 8) {
+        int32_t ends[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          ends[i] = all[min(g0 + i, a.groups - 1)];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          asm volatile("" : "+s"(ends[i]));   // (all on their way before the first is waited for)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (g < 0) {
+            run = max(run, ends[i]);
+            first += (int32_t)pg, part += (hi - lo + 127) / 128 * 128;
+            lo = hi, hi = min(run, (int32_t)a.m);
+            trows = (uint32_t)(hi - lo + TILE - 1) / TILE, pg = (trows * a.tiles_n + 7) / 8;
+            if ((uint32_t)(q - first) < pg)
+              g = g0 + i;
+          }
+        }
+      }
+      const uint32_t idx = (uint32_t)x * pg + (uint32_t)(q - first);
+      if (g < 0 || idx >= trows * a.tiles_n)
+        return false;
+      band_tile(idx, trows, tm);
+      p.group = g;
+      p.row0 = lo + (int32_t)tm * TILE;
+      p.rows = min(TILE, hi - (int32_t)p.row0);
+      p.srow0 = part + (int32_t)tm * TILE;
+      return true;
+    }
     GroupTable& table = *reinterpret_cast<GroupTable*>(lds);
     int32_t* xs = reinterpret_cast<int32_t*>(lds + sizeof(GroupTable));
     if (threadIdx.x < 64) {
-      if (a.groups <= kScalarTableGroups)
-        build_group_table_scalar(a.ends, a.groups, (int32_t)a.m, TILE, table);
-      else
-        build_group_table(a.ends, a.groups, (int32_t)a.m, TILE, table);
+      build_group_table(a.ends, a.groups, (int32_t)a.m, TILE, table);
       build_piece_starts(table, a.groups, TILE, a.tiles_n, xs);
     }
     lds_barrier();
-    const int32_t q = (int32_t)(blockIdx.x / 8), x = (int32_t)(blockIdx.x % 8);
     if (q >= __builtin_amdgcn_readfirstlane(xs[a.groups]))
       return false;
     int glo = 0, ghi = a.groups;   // xs[glo] <= q < xs[ghi]
