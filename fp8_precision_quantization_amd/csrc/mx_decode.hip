@@ -211,11 +211,12 @@ __global__ __launch_bounds__(64 * KS) void decode_kernel(DecodeArgs a) {
 }
 
 // Two blocks of 16 rows of W to a workgroup (half the reads of x that one
-// makes), two buffers to a wave, eight waves or as many as LDS holds.  Timed
-// (MXFP4, us): 1 x 8192 x 5120 6.7 (one block 8.1, four waves 7.2, four blocks
-// 7.9), 32 x 8192 x 5120 9.7 (one block 14.6, three buffers 10.0), 33 x 5120 x
-// 8192 15.9 (one block 25.7, two waves 22), 64 x 5120 x 8192 19.8 (two waves
-// 33).
+// makes), two buffers to a wave, eight waves for up to 16 rows of x and four (or
+// what LDS holds) above: one or two to a SIMD.  Timed (MXFP4, us): 1 x 8192 x
+// 5120 6.7, 3.3 TB/s (one block 8.1, four waves 7.2, four blocks 7.9), 32 x 8192
+// x 5120 9.4 (one block 14.6, three buffers 10.0, seven waves 10.9), 33 x 5120 x
+// 8192 14.7 (one block 25.7, two waves 22, five 14.6), 64 x 5120 x 8192 18.6 (two
+// waves 33): from 33 rows on x is four times the bytes of the workgroup's W.
 template <int FW, int TB, bool GATED>
 static void launch(const DecodeArgs& a, hipStream_t stream) {
   constexpr int RB = GATED ? 1 : 2, kBufs = 2;

@@ -153,7 +153,7 @@ mx_status mx_gated_ffn_decode(const void* x, int64_t ldx, const uint8_t* qw, con
 mx_status mx_gated_ffn(const uint8_t* qx, const uint8_t* sx, int32_t x_format, const uint8_t* qw, const uint8_t* sw,
                        int32_t w_format, const int32_t* group_end_offsets, int32_t num_groups, int64_t rows,
                        int64_t cols, int64_t k, int32_t act, void* y, uint8_t* q, uint8_t* s, hipStream_t stream) {
-  if (cols > kMaxCols)
+  if (cols < 0 || cols > kMaxCols)
     return MX_ERR_SHAPE;
   const mx_status st = check_ffn(x_format, w_format, group_end_offsets, num_groups, rows, cols, 2 * cols, k, act);
   if (st != MX_OK)
