@@ -48,7 +48,11 @@ typedef int v8i __attribute__((ext_vector_type(8)));
 typedef float v16f __attribute__((ext_vector_type(16)));
 
 constexpr int kMmK = 128;     // K of a stage
-constexpr int kMmBand = 8;    // tile rows to a band of the tile order
+// Tile rows to a band of the tile order (the 32 CUs of an XCD then work on 5 x 6
+// tiles or so; us, of 4, 5, 6, 7, 8: block 16640 x 4096 x 5120 in MXFP8 645, 567, 603,
+// 568, 586-633, its gradient 405, 364, 377, 381, 371-377, block 32768 x 2048 x 2048
+// -, 271, 279, 273, 290).
+constexpr int kMmBand = 5;
 
 // Codes of a format: what the MFMA calls it, bytes of a stage's row.
 template <int FMT>
@@ -140,7 +144,7 @@ struct MmPlace {
 
 // The tile of this workgroup: false if it has none (uniform; no barrier is
 // left open).  XCD x (workgroups are dealt to the XCDs in turn) owns one of 8
-// contiguous pieces of the ordered tiles: bands of 8 tile rows, column by
+// contiguous pieces of the ordered tiles: bands of kMmBand tile rows, column by
 // column.  Grouped: a piece of each group's tiles, group after group.  `lds`
 // holds the table of many groups meanwhile.
 template <bool GROUPED, int TILE>
