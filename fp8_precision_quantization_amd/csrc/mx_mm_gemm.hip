@@ -48,7 +48,7 @@ __device__ __forceinline__ void store_c(const MmArgs& a, const MmPlace& p, int64
     mm_wave_fence();
     E* dst = c + (p.row0 + row0 + 32 * j) * a.n + c0;
     if (words)
-      st.template drain<kCacheNT>(reinterpret_cast<uint8_t*>(dst), a.n * (int)sizeof(E), rows, n * (int)sizeof(E));
+      st.drain(reinterpret_cast<uint8_t*>(dst), a.n * (int)sizeof(E), rows, n * (int)sizeof(E));
     else
       st.drain_each(dst, a.n, rows, n);
     mm_wave_fence();
