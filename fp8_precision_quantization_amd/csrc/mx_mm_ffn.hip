@@ -12,16 +12,17 @@
 // codes of the same tile come through LDS; dg = dy u act'(g), du = dy act(g).
 //
 // Timed at 16640 rows, 4096 columns, k 5120 (us): block in MXFP8 with the
-// checkpoint 580-640 (2.2-2.4 PFLOP/s), MXFP8 rows and MXFP4 weights 570-600, in
-// MXFP4 420-445; gradient in MXFP8 375-395, in MXFP4 with y again 310-325.
-// Without their epilogues these take 536, 493, 335, 280 and 181: a workgroup has
-// a CU to itself (its sums are half of the CU's registers), so nothing covers an
-// epilogue, 300 to 540 KB of loads and stores a tile.  Two workgroups of 128 x
-// 128 a CU cover each other's, but load each operand twice as often: 710 for
-// the block, 432 for its gradient in MXFP8.  Four waves of 128 x 128 to a large
-// tile, as the products take them, leave one wave a SIMD to run the epilogue:
-// 626 and 417.  Of the rest, a stage of MXFP8 moves 256 KB through a CU's LDS,
-// 2048 cycles at 128 bytes each, and keeps its MFMAs busy as long.
+// checkpoint 550-605 (2.3-2.5 PFLOP/s), MXFP8 rows and MXFP4 weights 550-575, in
+// MXFP4 390-405; gradient in MXFP8 362-380, in MXFP4 with y again 297-305.
+// Epilogues are 45, 75, 90, 95 and 130 of these: a workgroup has a CU to itself
+// (its sums are half of the CU's registers), so nothing covers an epilogue, 300
+// to 540 KB of loads and stores a tile.  Two workgroups of 128 x 128 a CU cover
+// each other's, but load each operand twice as often: 710 for the block, 432 for
+// its gradient in MXFP8, where large tiles took 585 and 376.  Four waves of 128 x
+// 128 to a large tile, as the products take them, leave one wave a SIMD to run
+// the epilogue: 626 and 417 then.  Of the rest, a stage of MXFP8 moves 256 KB
+// through a CU's LDS, 2048 cycles at 128 bytes each, and keeps its MFMAs busy as
+// long.
 #include "mx_gate.h"
 #include "mx_mm_out.h"
 
