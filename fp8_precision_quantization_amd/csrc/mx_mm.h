@@ -48,6 +48,11 @@ typedef int v8i __attribute__((ext_vector_type(8)));
 typedef float v16f __attribute__((ext_vector_type(16)));
 
 constexpr int kMmK = 128;     // K of a stage
+// Most tiles of an XCD's last round that are taken in quarters (us, whole and in
+// quarters: 4 tiles, 16640 x 8192 x 5120 in MXFP4 356 and 343, gradient of 16640 x
+// 4096 x 5120 in MXFP8 366 and 338; 5 tiles, 4352 x 4352 x 4096 60 and 48; 12 tiles,
+// 5632 x 4096 x 4096 62.0 and 60.1; 16 tiles, 6144 x 4096 x 4096 63.1 and 61.3).
+constexpr int kMmSplit = 16;
 // Tile rows to a band of the tile order (the 32 CUs of an XCD then work on 5 x 6
 // tiles or so; us, of 4, 5, 6, 7, 8: block 16640 x 4096 x 5120 in MXFP8 645, 567, 603,
 // 568, 586-633, its gradient 405, 364, 377, 381, 371-377, block 32768 x 2048 x 2048
@@ -71,27 +76,30 @@ __device__ __forceinline__ int mm_swizzle(int row) {
 
 // Tiles.  Large: 256 x 256, by eight waves, two to a SIMD, or WIDE by four of
 // 128 x 128 each, which read a third less from LDS but leave an epilogue fewer
-// registers.  Small: 128 x 128 by four, two workgroups to a CU.
-template <int FX, int FW, bool LARGE, bool WIDE = false>
+// registers.  Small: 128 x 128 by four, two workgroups to a CU, or EIGHT by eight
+// of 32 x 64, a quarter of a large tile in a launch of these.
+template <int FX, int FW, bool LARGE, bool WIDE = false, bool EIGHT = false>
 struct MmTile {
-  static constexpr int kBX = WIDE ? 4 : 2, kBW = LARGE ? 4 : 2, kWX = LARGE && !WIDE ? 4 : 2, kWW = 2;
-  static constexpr int kPerCu = LARGE ? 1 : 2, kWavesPerSimd = WIDE ? 1 : 2;
+  static constexpr int kBX = WIDE ? 4 : EIGHT ? 1 : 2, kBW = LARGE ? 4 : 2;
+  static constexpr int kWX = (LARGE && !WIDE) || EIGHT ? 4 : 2, kWW = 2;
+  static constexpr int kPerCu = LARGE || EIGHT ? 1 : 2;
   static constexpr int kWaves = kWX * kWW, kThreads = 64 * kWaves;
   static constexpr int kRowsX = 32 * kBX * kWX, kRowsW = 32 * kBW * kWW;
   static constexpr int kX = 0;
   static constexpr int kW = kRowsX * MmFormat<FX>::kRow;
   static constexpr int kSX = kW + kRowsW * MmFormat<FW>::kRow;   // scales: 4 bytes a row
   static constexpr int kSW = kSX + kRowsX * 4;
-  static constexpr int kSlot = kSW + kRowsW * 4;
+  static constexpr int kLoadsS = (kRowsX + kRowsW + 64 * kWaves - 1) / 64 / kWaves;   // of scales, 256 bytes each
+  static constexpr int kSlot = kSX + kLoadsS * kWaves * 256;   // (of eight waves' loads the last four may be for none)
   // as many slots as a workgroup's share of a CU's LDS holds, four at most
   static constexpr int kFit = 163840 / kPerCu / kSlot;
   static constexpr int kSlots = kFit > 4 ? 4 : kFit;
   static constexpr int kLds = kSlots * kSlot;
   static constexpr int kLoadsX = kW / (1024 * kWaves);   // loads of a wave, 1 KiB each
   static constexpr int kLoadsW = (kSX - kW) / (1024 * kWaves);
-  static constexpr int kLoadsS = (kRowsX + kRowsW) / 64 / kWaves;   // of scales, 256 bytes each
   static constexpr int kLoads = kLoadsX + kLoadsW + kLoadsS;
-  static_assert(kLoadsS * kWaves * 64 == kRowsX + kRowsW && kRowsX % 64 == 0, "a load's scales are one operand's");
+  static_assert(kLoadsS * kWaves * 64 >= kRowsX + kRowsW && kRowsX % 64 == 0 && kRowsW % 64 == 0,
+                "a load's scales are one operand's");
   static_assert(kSlots >= 2 && (kSlots - 1) * kLoads < 64, "slots and the load counter");
 };
 
@@ -102,6 +110,7 @@ struct MmArgs {
   int32_t groups;
   int64_t w_bytes, sw_bytes;   // codes and scales of one group's W
   uint32_t tiles_m, tiles_n, per_xcd;
+  uint32_t split;              // of each XCD's tiles the last that are taken in quarters
 };
 
 // 16 or 4 bytes a lane from memory to LDS at `to` (the wave's; lane order).
@@ -140,6 +149,7 @@ struct MmPlace {
   int64_t srow0;      // its first row in X's scale layout, a multiple of 128
   uint32_t tn;        // its tile column
   int32_t group;
+  int32_t quarter;    // 0 to 3 of the tile, or -1: all of it
 };
 
 // The tile of this workgroup: false if it has none (uniform; no barrier is
@@ -158,8 +168,15 @@ __device__ __forceinline__ bool mm_place(const MmArgs& a, uint8_t* lds, MmPlace&
   };
   uint32_t tm;
   if constexpr (!GROUPED) {
-    const uint32_t id = (blockIdx.x % 8) * a.per_xcd + blockIdx.x / 8;
-    if (blockIdx.x / 8 >= a.per_xcd || id >= a.tiles_m * a.tiles_n)
+    uint32_t i = blockIdx.x / 8;
+    const uint32_t whole = a.per_xcd - a.split;
+    p.quarter = -1;
+    if (i >= whole) {
+      p.quarter = (int32_t)((i - whole) % 4);
+      i = whole + (i - whole) / 4;
+    }
+    const uint32_t id = (blockIdx.x % 8) * a.per_xcd + i;
+    if (i >= a.per_xcd || id >= a.tiles_m * a.tiles_n)
       return false;
     band_tile(id, a.tiles_m, tm);
     p.group = 0;
@@ -251,6 +268,15 @@ __device__ __forceinline__ bool mm_place(const MmArgs& a, uint8_t* lds, MmPlace&
   }
 }
 
+// A quarter of the place: its first column, and whether it holds anything.
+// tile, cols: rows and columns of R of the whole tile.
+__device__ __forceinline__ bool mm_quarter(const MmArgs& a, MmPlace& p, int tile, int64_t& col0, int cols) {
+  const int down = p.quarter / 2 * (tile / 2);
+  p.row0 += down, p.srow0 += down, p.rows = min(tile / 2, p.rows - down);
+  col0 += p.quarter % 2 * (cols / 2);
+  return p.rows > 0 && col0 < a.n;
+}
+
 // The tile's accumulators: acc[i][j] is the block of W rows 32 i and X rows
 // 32 j of this wave's part, wave w's at (w / WW, w % WW).  GATED: the wave's W
 // rows are 16 BW rows from its columns' gate half and the same of the factor
@@ -314,6 +340,8 @@ __device__ __forceinline__ void mm_tile(const MmArgs& a, const MmPlace& p, int64
       row += col0 - scol0;
     }
     soff[u] = (uint32_t)(row / 128 * strip + 16 * (row % 32) + 4 * (row % 128 / 32));
+    if (u * T::kWaves + wave >= (T::kRowsX + T::kRowsW) / 64)
+      soff[u] = 0, rs[u] = buffer_rsrc(a.sw, 0);
   }
 
   // load i of stage t into slot b: X, W, scales
@@ -497,12 +525,15 @@ inline bool mm_large(int64_t m, int64_t n, int32_t groups, int tile_cols) {
 }
 
 // Tiles of a launch, and its workgroups.  cols_tile: columns of R to a tile.
-inline int64_t mm_grid(MmArgs& a, int tile, int cols_tile) {
+// A workgroup with a large tile has a CU to itself, and an XCD 32 of them: where
+// few of an XCD's tiles are left after whole rounds, these are taken in quarters.
+inline int64_t mm_grid(MmArgs& a, int tile, int cols_tile, bool quarters = false) {
   const int64_t groups = a.ends != nullptr ? a.groups : 0;
   const int64_t tm = (a.m + tile - 1) / tile + groups, tn = (a.n + cols_tile - 1) / cols_tile;
   const int64_t per = (tm * tn + 7) / 8 + groups;
   a.tiles_m = (uint32_t)tm, a.tiles_n = (uint32_t)tn, a.per_xcd = (uint32_t)per;
-  return per * 8;
+  a.split = quarters && groups == 0 && per > 32 && per % 32 <= kMmSplit ? (uint32_t)(per % 32) : 0;
+  return (per + 3 * a.split) * 8;
 }
 
 }  // namespace mx

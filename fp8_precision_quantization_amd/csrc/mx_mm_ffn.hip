@@ -12,8 +12,8 @@
 // codes of the same tile come through LDS; dg = dy u act'(g), du = dy act(g).
 //
 // Timed at 16640 rows, 4096 columns, k 5120 (us): block in MXFP8 with the
-// checkpoint 550-605 (2.3-2.5 PFLOP/s), MXFP8 rows and MXFP4 weights 550-575, in
-// MXFP4 390-405; gradient in MXFP8 362-380, in MXFP4 with y again 297-305.
+// checkpoint 538-590 (2.4-2.6 PFLOP/s), MXFP8 rows and MXFP4 weights 535-560, in
+// MXFP4 383-395; gradient in MXFP8 338-354, in MXFP4 with y again 276-288.
 // Epilogues are 45, 75, 90, 95 and 130 of these: a workgroup has a CU to itself
 // (its sums are half of the CU's registers), so nothing covers an epilogue, 300
 // to 540 KB of loads and stores a tile.  Two workgroups of 128 x 128 a CU cover
@@ -137,15 +137,37 @@ __device__ __forceinline__ void ffn_store(const MmArgs& a, const FfnArgs& o, con
   }
 }
 
+// Tiles, and the quarters of the last ones in a launch of large tiles.
+template <int FX, int FW>
+using FfnQuarter = MmTile<FX, FW, false, false, true>;
+template <int FX, int FW, bool LARGE, bool GROUPED>
+constexpr int kFfnLds = LARGE && !GROUPED && FfnQuarter<FX, FW>::kLds > MmTile<FX, FW, LARGE>::kLds
+                            ? FfnQuarter<FX, FW>::kLds
+                            : MmTile<FX, FW, LARGE>::kLds;
+
 template <int FX, int FW, bool LARGE, bool GROUPED>
 __global__ __launch_bounds__(LARGE ? 512 : 256) __attribute__((amdgpu_waves_per_eu(2, 2)))
 void ffn_kernel(MmArgs a, FfnArgs o) {
   using T = MmTile<FX, FW, LARGE>;
-  __shared__ __attribute__((aligned(256))) uint8_t lds[T::kLds];
+  __shared__ __attribute__((aligned(256))) uint8_t lds[kFfnLds<FX, FW, LARGE, GROUPED>];
   MmPlace p;
   if (!mm_place<GROUPED, T::kRowsX>(a, lds, p))
     return;
-  const int64_t col0 = (int64_t)p.tn * (T::kRowsW / 2);
+  int64_t col0 = (int64_t)p.tn * (T::kRowsW / 2);
+  if constexpr (LARGE && !GROUPED) {
+    if (p.quarter >= 0) {
+      using Q = FfnQuarter<FX, FW>;
+      if (!mm_quarter(a, p, T::kRowsX, col0, T::kRowsW / 2))
+        return;
+      v16f acc[Q::kBW][Q::kBX];
+      mm_tile<FX, FW, Q, true>(a, p, col0, lds, acc);
+      if (o.gelu)
+        ffn_store<Q, true>(a, o, p, col0, lds, acc);
+      else
+        ffn_store<Q, false>(a, o, p, col0, lds, acc);
+      return;
+    }
+  }
   v16f acc[T::kBW][T::kBX];
   mm_tile<FX, FW, T, true>(a, p, col0, lds, acc);
   if (o.gelu)
@@ -273,13 +295,27 @@ template <int FX, int FW, bool LARGE, bool GROUPED>
 __global__ __launch_bounds__(LARGE ? 512 : 256) __attribute__((amdgpu_waves_per_eu(2, 2)))
 void ffn_bwd_kernel(MmArgs a, FfnArgs o) {
   using T = MmTile<FX, FW, LARGE>;
-  __shared__ __attribute__((aligned(256))) uint8_t lds[T::kLds];
+  __shared__ __attribute__((aligned(256))) uint8_t lds[kFfnLds<FX, FW, LARGE, GROUPED>];
   static_assert(T::kWaves * 2 * Staged<32 * T::kBW>::kSize <= T::kLds &&
                 T::kWaves * Staged<64 * T::kBW>::kSize <= T::kLds, "the epilogue's rows");
   MmPlace p;
   if (!mm_place<GROUPED, T::kRowsX>(a, lds, p))
     return;
-  const int64_t col0 = (int64_t)p.tn * T::kRowsW;
+  int64_t col0 = (int64_t)p.tn * T::kRowsW;
+  if constexpr (LARGE && !GROUPED) {
+    if (p.quarter >= 0) {
+      using Q = FfnQuarter<FX, FW>;
+      if (!mm_quarter(a, p, T::kRowsX, col0, T::kRowsW))
+        return;
+      v16f acc[Q::kBW][Q::kBX];
+      mm_tile<FX, FW, Q, false>(a, p, col0, lds, acc);
+      if (o.gelu)
+        ffn_bwd_store<Q, true>(a, o, p, col0, lds, acc);
+      else
+        ffn_bwd_store<Q, false>(a, o, p, col0, lds, acc);
+      return;
+    }
+  }
   v16f acc[T::kBW][T::kBX];
   mm_tile<FX, FW, T, false>(a, p, col0, lds, acc);
   if (o.gelu)
@@ -322,7 +358,7 @@ static hipError_t launch_either(bool bwd, const MmOperands& in, int64_t m, int64
   const bool large = mm_large(m, n, in.groups, bwd ? 256 : 128);
   MmArgs a = mm_args(in, m, n, bwd ? n : 2 * n, k);
   const int tile = large ? 256 : 128;
-  const dim3 grid((unsigned)mm_grid(a, tile, bwd ? tile : tile / 2));
+  const dim3 grid((unsigned)mm_grid(a, tile, bwd ? tile : tile / 2, large));
   if (large)
     launch_formats<true>(bwd, in.x_format, in.w_format, a, o, grid, stream);
   else

@@ -2,9 +2,9 @@
 // MXFP4 or MXFP8, B in MXFP4, dense or grouped along M (mx_mm.h has the
 // product itself).
 //
-// Timed (us): 16640 x 8192 x 5120 in MXFP4, bf16 out, 352-390 (3.6-4.0
+// Timed (us): 16640 x 8192 x 5120 in MXFP4, bf16 out, 340-380 (3.7-4.1
 // PFLOP/s; the MFMAs alone, fed the same codes from registers, take 237 and hold
-// the clock at 1.4-1.6 GHz), with MXFP8 rows 500-530 (2.7; the MFMAs alone 3.0);
+// the clock at 1.4-1.6 GHz), with MXFP8 rows 489-520 (2.8; the MFMAs alone 3.0);
 // 16640 x 2048 x 5120 in 16 groups with MXFP8 rows 170-187.  Bound by power: the
 // clock is 1.75-1.8 GHz with the MFMAs busy 49% of the cycles, and 2.2 where
 // nothing is loaded.  Large tiles by four waves of 128 x 128 read a third less
@@ -67,7 +67,21 @@ void mm_gemm_kernel(MmArgs a, MmGemmOut o) {
   MmPlace p;
   if (!mm_place<GROUPED, T::kRowsX>(a, lds, p))
     return;
-  const int64_t col0 = (int64_t)p.tn * T::kRowsW;
+  int64_t col0 = (int64_t)p.tn * T::kRowsW;
+  if constexpr (LARGE && !GROUPED) {
+    if (p.quarter >= 0) {
+      using Q = GemmTile<FX, false>;
+      if (!mm_quarter(a, p, T::kRowsX, col0, T::kRowsW))
+        return;
+      v16f acc[Q::kBW][Q::kBX];
+      mm_tile<FX, MX_FORMAT_E2M1, Q, false>(a, p, col0, lds, acc);
+      if (o.f32)
+        store_c<Q>(a, p, col0, lds, o.words, static_cast<float*>(o.c), acc);
+      else
+        store_c<Q>(a, p, col0, lds, o.words, static_cast<uint16_t*>(o.c), acc);
+      return;
+    }
+  }
   v16f acc[T::kBW][T::kBX];
   mm_tile<FX, MX_FORMAT_E2M1, T, false>(a, p, col0, lds, acc);
   if (o.f32)
@@ -95,7 +109,7 @@ int64_t gemm4_grid_blocks(int64_t m, int64_t n, int32_t groups) {
 hipError_t launch_gemm4(const MmOperands& in, int64_t m, int64_t n, int64_t k, void* c, bool f32, hipStream_t stream) {
   const bool large = mm_large(m, n, in.groups, 256);
   MmArgs a = mm_args(in, m, n, n, k);
-  const dim3 grid((unsigned)mm_grid(a, large ? 256 : 128, large ? 256 : 128));
+  const dim3 grid((unsigned)mm_grid(a, large ? 256 : 128, large ? 256 : 128, large));
   const MmGemmOut o = {c, f32, n * (f32 ? 4 : 2) % 16 == 0 && (uintptr_t)c % 16 == 0};
   if (in.x_format == MX_FORMAT_E2M1) {
     if (large)

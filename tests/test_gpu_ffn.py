@@ -162,14 +162,25 @@ def test_backward_grouped(rows, f, k, ends, fx, fw, oracle_mod):
 @pytest.mark.parametrize("fx,fw", PAIRS)
 def test_large_tiles(fx, fw, oracle_mod):
     """Enough tiles that the larger ones are taken, with ragged edges."""
+    _large(fx, fw, (4100, 1568, 160), (3333, 3680, 96), oracle_mod)
+
+
+@pytest.mark.parametrize("fx,fw", PAIRS)
+@pytest.mark.parametrize("forward,backward", [((4100, 2112, 96), (4100, 4128, 160)), ((5001, 2080, 288), (4353, 4096, 32))])
+def test_last_tiles_in_quarters(forward, backward, fx, fw, oracle_mod):
+    """A few tiles more than whole rounds of them, cut at either edge."""
+    _large(fx, fw, forward, backward, oracle_mod)
+
+
+def _large(fx, fw, forward, backward, oracle_mod):
     dev = device()
-    rows, f, k = 4100, 1568, 160
+    rows, f, k = forward
     rng = np.random.default_rng(11)
     args, _, x, w = _operands(oracle_mod, rng, dev, rows, 2 * f, k, fx, fw, None)
     kw = dict(act="silu", a_format=NAMES[fx], w_format=NAMES[fw])
     y, q, s = mx.mx_gated_ffn(*args, raw=True, **kw)
     _check_forward(y, q, s, x, w[0], fx, fw, "silu", "large")
-    rows, f, k = 3333, 3680, 96
+    rows, f, k = backward
     args, _, d, w = _operands(oracle_mod, rng, dev, rows, f, k, fx, fw, None)
     q, s, h = _kept(rng, rows, f)
     dh, y = mx.mx_gated_ffn_backward(*args, to_dev_u8(q, dev), to_dev_u8(s, dev), recompute=True, **kw)

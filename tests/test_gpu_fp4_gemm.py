@@ -63,6 +63,12 @@ def test_large_tiles(m, n, k, fa, oracle_mod):
         assert torch.equal(c, mx.mx_gemm_mxfp4(*args, out_dtype=dt))
 
 
+@pytest.mark.parametrize("m,n,k,fa", [(4100, 4301, 160, "e2m1"), (5000, 4200, 96, "e4m3"), (4353, 4096, 544, "e2m1")])
+def test_last_tiles_in_quarters(m, n, k, fa, oracle_mod):
+    """A few tiles more than whole rounds of them, cut at either edge."""
+    test_large_tiles(m, n, k, fa, oracle_mod)
+
+
 def _grouped(oracle_mod, rng, dev, m, n, k, fa, ends):
     g = len(ends)
     qa, sa = r4.operand(rng, m, k, fa)
