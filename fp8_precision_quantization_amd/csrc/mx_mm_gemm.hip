@@ -6,7 +6,7 @@
 // PFLOP/s; the MFMAs alone, fed the same codes from registers, take 237 and hold
 // the clock at 1.4-1.6 GHz), with MXFP8 rows 489-520 (2.8; the MFMAs alone 3.0);
 // 16640 x 2048 x 5120 in 16 groups with MXFP8 rows 170-187.  Bound by power: the
-// clock is 1.75-1.8 GHz with the MFMAs busy 49% of the cycles, and 2.2 where
+// clock is 1.75-1.8 GHz with the MFMAs busy 51% of the cycles, and 2.2 where
 // nothing is loaded.  Large tiles by four waves of 128 x 128 read a third less
 // from LDS than by eight (375 against 360), and here the epilogue is short.
 #include "mx_fp4_launch.h"
