@@ -75,9 +75,14 @@ MX_API mx_status mx_dequantize_mxfp4(const uint8_t* q, const uint8_t* s, int64_t
  *   qb, sb   B's MXFP4 codes (n, k / 2) and blocked scales; 16-byte aligned.
  *   c        (m, n) of c_type, its element's alignment (16-byte, with rows of
  *            whole 16-byte words, is faster).
- * With A in MXFP4 every step of the sum is binary32's; with A in MXFP8 a
- * 64-deep step is summed with less (within 4e-4 of its largest product, as in
- * mx_gemm_mxfp8).  A NaN code or scale gives NaN where it enters.
+ * With A in MXFP4 every step of the sum is binary32's.  With A in MXFP8 the
+ * matrix instruction adds the products of eight neighbouring k, from a multiple
+ * of eight on, with fewer bits, as in mx_gemm_mxfp8: each is cut toward zero to a
+ * multiple of 2^-13 times the largest 2^(ea + eb) among those that are not zero
+ * (ea, eb the exponents of the codes' fields, before the scales; a subnormal code
+ * has its format's lowest), which takes less than that unit from each but the
+ * largest.  The groups of eight meet in binary32.  A NaN code or scale gives NaN
+ * where it enters.
  * m, n, k >= 0, k % 32 == 0, k <= 2^23, n <= 2^24, n * k < 2^36, m < 2^31 and
  * the tiles of a launch, else MX_ERR_SHAPE; m or n 0 writes nothing; k 0
  * writes zeros.
@@ -130,9 +135,9 @@ MX_API mx_status mx_linear_decode(const void* x, int64_t ldx, const uint8_t* qw,
  *   q, s     the 8-bit checkpoint of (g, u), as mx_gated_act writes it of a
  *            bf16 h, here of the binary32 sums: codes (rows, 2 * cols), 16-byte
  *            aligned, and plain scales (rows, 2 * cols / 32); or both NULL.
- * Sums as for mx_gemm_mxfp4: with an MXFP8 operand a 64-deep step is within
- * 4e-4 of its largest product, so that a few of the checkpoint's codes (of
- * numbers next to the middle of two) are the neighbour of what exact sums give.
+ * Sums as for mx_gemm_mxfp4: with an MXFP8 operand products are cut before they
+ * are added, so that a few of the checkpoint's codes (of numbers next to the
+ * middle of two) are the neighbour of what exact sums give.
  * rows, cols, k >= 0; cols and k multiples of 32; k <= 2^23, cols <= 2^24, 2 *
  * cols * k < 2^36, rows + 256 * num_groups < 2^31, else MX_ERR_SHAPE.
  */
