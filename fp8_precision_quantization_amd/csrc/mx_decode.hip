@@ -69,15 +69,15 @@ __global__ __launch_bounds__(64 * KS) void decode_kernel(DecodeArgs a) {
   // time (which may lie far apart): rows past the end, and K past it (an offset
   // outside), read as zeros.
   const int64_t rows = min((int64_t)16 * RB, a.n - j0), up = GATED ? a.n : 0;
-  const __amdgpu_buffer_rsrc_t rw = buffer_rsrc(a.qw + j0 * ldw, (uint32_t)(rows * ldw));
-  const __amdgpu_buffer_rsrc_t ru = GATED ? buffer_rsrc(a.qw + (j0 + up) * ldw, (uint32_t)(rows * ldw)) : rw;
+  const MmRange rw = mm_range(a.qw + j0 * ldw, (uint32_t)(rows * ldw));
+  const MmRange ru = GATED ? mm_range(a.qw + (j0 + up) * ldw, (uint32_t)(rows * ldw)) : rw;
   auto four_rows = [&](int u) {
     const int rows = min(4, a.m - 4 * u);
-    return buffer_rsrc(a.x + (rows > 0 ? 4 * u * a.ldx : 0), rows > 0 ? (uint32_t)(((rows - 1) * a.ldx + a.k) * 2) : 0u);
+    return mm_range(a.x + (rows > 0 ? 4 * u * a.ldx : 0), rows > 0 ? (uint32_t)(((rows - 1) * a.ldx + a.k) * 2) : 0u);
   };
   // scale words: lane l's is of W's row l of the workgroup's, gate's rows first
   const int64_t srow0 = j0 / 128 * 128, srows = (a.n + up + 127) / 128 * 128 - srow0;
-  const __amdgpu_buffer_rsrc_t rs = buffer_rsrc(a.sw + srow0 / 128 * strip, (uint32_t)(srows / 128 * strip));
+  const MmRange rs = mm_range(a.sw + srow0 / 128 * strip, (uint32_t)(srows / 128 * strip));
   uint32_t soff;
   {
     const int64_t row = j0 - srow0 + lane % (16 * RB) + (lane >= 16 * RB ? up : 0);

@@ -122,20 +122,35 @@ struct MmArgs {
   uint32_t split;              // of each XCD's tiles the last that are taken in quarters
 };
 
-// 16 or 4 bytes a lane from memory to LDS at `to` (the wave's; lane order).
-template <int BYTES>
-__device__ __forceinline__ void mm_load(uint32_t to, __amdgpu_buffer_rsrc_t rsrc, uint32_t offset) {
-  static_assert(BYTES == 16 || BYTES == 4, "load sizes");
-  // (a write of m0 and its use by a load to LDS need an instruction between)
-  if constexpr (BYTES == 16)
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(to), "v"(offset),
-                 "s"(rsrc)
-                 : "memory");
-  else
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(to), "v"(offset),
-                 "s"(rsrc)
-                 : "memory");
+// A buffer range [base, base + bytes) for mm_load, as the halves of its descriptor.
+struct MmRange {
+  uint64_t lo, hi;
+};
+__device__ __forceinline__ MmRange mm_range(const void* base, uint32_t bytes) {
+  return {(uint64_t)(uintptr_t)base, (uint64_t)0x00020000u << 32 | bytes};   // (the raw-buffer format of buffer_rsrc())
 }
+
+// 16 or 4 bytes a lane from memory to LDS at `to` (the wave's; lane order).  The
+// compiler does not look into the asm for hazards.  A load may follow a write of
+// its descriptor by the vector unit (v_readlane, v_readfirstlane: also where the
+// compiler restores a spilled register) by five wait states at the earliest, but
+// one by the scalar unit at once: the block copies the descriptor, which is also
+// what has to stand between the write of m0 and the load.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"   // (m0 is reserved, and none of the compiler's own writes of it may move across)
+template <int BYTES>
+__device__ __forceinline__ void mm_load(uint32_t to, const MmRange& range, uint32_t offset) {
+  static_assert(BYTES == 16 || BYTES == 4, "load sizes");
+  if constexpr (BYTES == 16)
+    asm volatile("s_mov_b32 m0, %0\n\ts_mov_b64 s[92:93], %2\n\ts_mov_b64 s[94:95], %3\n\t"
+                 "buffer_load_dwordx4 %1, s[92:95], 0 offen lds" ::"s"(to), "v"(offset), "s"(range.lo), "s"(range.hi)
+                 : "memory", "m0", "s92", "s93", "s94", "s95");
+  else
+    asm volatile("s_mov_b32 m0, %0\n\ts_mov_b64 s[92:93], %2\n\ts_mov_b64 s[94:95], %3\n\t"
+                 "buffer_load_dword %1, s[92:95], 0 offen lds" ::"s"(to), "v"(offset), "s"(range.lo), "s"(range.hi)
+                 : "memory", "m0", "s92", "s93", "s94", "s95");
+}
+#pragma clang diagnostic pop
 
 // Until at most N of the wave's loads are in flight.
 template <int N>
@@ -306,13 +321,13 @@ __device__ __forceinline__ void mm_tile(const MmArgs& a, const MmPlace& p, int64
   const int strip = (int)((a.k / 32 + 3) / 4) * 512;   // a 128-row strip of a scale layout
   const int stages = (int)((a.k + kMmK - 1) / kMmK);
 
-  const __amdgpu_buffer_rsrc_t rx = buffer_rsrc(a.qx + p.row0 * ldx, (uint32_t)p.rows * (uint32_t)ldx);
+  const MmRange rx = mm_range(a.qx + p.row0 * ldx, (uint32_t)p.rows * (uint32_t)ldx);
   // W: one range, or the gate's and the factor's
   constexpr int kCols = GATED ? T::kRowsW / 2 : T::kRowsW;
   const int cols = (int)min((int64_t)kCols, a.n - col0);
   const uint8_t* wbase = a.qw + p.group * a.w_bytes + col0 * ldw;
-  const __amdgpu_buffer_rsrc_t rw = buffer_rsrc(wbase, (uint32_t)cols * (uint32_t)ldw);
-  const __amdgpu_buffer_rsrc_t ru = GATED ? buffer_rsrc(wbase + a.n * ldw, (uint32_t)cols * (uint32_t)ldw) : rw;
+  const MmRange rw = mm_range(wbase, (uint32_t)cols * (uint32_t)ldw);
+  const MmRange ru = GATED ? mm_range(wbase + a.n * ldw, (uint32_t)cols * (uint32_t)ldw) : rw;
 
   const uint32_t lds0 =
       __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds);
@@ -330,13 +345,13 @@ __device__ __forceinline__ void mm_tile(const MmArgs& a, const MmPlace& p, int64
   // row's words of those blocks together.  Load u of wave w brings words 64 (u
   // * waves + w) on, X's first.
   const int64_t scol0 = col0 / 128 * 128;
-  __amdgpu_buffer_rsrc_t rs[T::kLoadsS];
+  MmRange rs[T::kLoadsS];
   uint32_t soff[T::kLoadsS];
 #pragma unroll
   for (int u = 0; u < T::kLoadsS; ++u) {
     const bool of_x = u * T::kWaves + wave < T::kRowsX / 64;
-    rs[u] = of_x ? buffer_rsrc(a.sx + p.srow0 / 128 * strip, (uint32_t)((p.rows + 127) / 128 * strip))
-                 : buffer_rsrc(a.sw + p.group * a.sw_bytes + scol0 / 128 * strip,
+    rs[u] = of_x ? mm_range(a.sx + p.srow0 / 128 * strip, (uint32_t)((p.rows + 127) / 128 * strip))
+                 : mm_range(a.sw + p.group * a.sw_bytes + scol0 / 128 * strip,
                                (uint32_t)(a.sw_bytes - scol0 / 128 * strip));
     const int d = threadIdx.x + u * T::kThreads - (of_x ? 0 : T::kRowsX), B = of_x ? BX : BW;
     int64_t row = 32 * B * (d / (32 * B)) + 32 * (d % B) + d / B % 32;   // in the scale layout, from the range's start
@@ -350,7 +365,7 @@ __device__ __forceinline__ void mm_tile(const MmArgs& a, const MmPlace& p, int64
     }
     soff[u] = (uint32_t)(row / 128 * strip + 16 * (row % 32) + 4 * (row % 128 / 32));
     if (u * T::kWaves + wave >= (T::kRowsX + T::kRowsW) / 64)
-      soff[u] = 0, rs[u] = buffer_rsrc(a.sw, 0);
+      soff[u] = 0, rs[u] = mm_range(a.sw, 0);
   }
 
   // load i of stage t into slot b: X, W, scales
