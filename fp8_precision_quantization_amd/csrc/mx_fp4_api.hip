@@ -13,6 +13,7 @@ constexpr int64_t kMaxK = (int64_t)1 << 23;             // a tile's row offsets 
 constexpr int64_t kMaxWeights = (int64_t)1 << 36;       // a group's scale offsets are 32 bits
 constexpr int64_t kMaxCols = (int64_t)1 << 24;          // and those of 32 rows of a result
 constexpr int64_t kMaxDecodeLd = (int64_t)1 << 28;      // and those of four rows of x
+constexpr int64_t kMaxDecodeCols = 16 * kMaxGridBlocks; // at least 16 columns to a workgroup
 constexpr int64_t kMaxCast = (int64_t)1 << 34;
 
 bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p % a) == 0; }
@@ -66,7 +67,7 @@ mx_status decode(const void* x, int64_t ldx, const uint8_t* qw, const uint8_t* s
     return MX_ERR_SHAPE;
   if (m == 0 || n == 0)
     return MX_OK;
-  if ((n + 15) / 16 > kMaxGridBlocks)
+  if (n > kMaxDecodeCols)
     return MX_ERR_SHAPE;
   if (c == nullptr || (k > 0 && (x == nullptr || qw == nullptr || sw == nullptr)))
     return MX_ERR_NULL;

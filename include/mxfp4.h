@@ -108,10 +108,12 @@ MX_API mx_status mx_grouped_gemm_mxfp4(const uint8_t* qa, const uint8_t* sa, int
  *   qw, sw   W's codes in w_format and blocked scales; 16-byte aligned.
  *   c        (m, n) of c_type, contiguous, its element's alignment.
  * x enters as it is; a code times its scale is exact in bf16 but for e4m3
- * values under scale bytes 0 to 2 (rounded to a multiple of 2^-133).
- * 0 <= m <= MX_MAX_DECODE_ROWS, n < 2^31, k % 32 == 0, 0 <= k <= 2^23, n * k <
- * 2^36, k <= ldx <= 2^28, else MX_ERR_SHAPE; m or n 0 writes nothing; k 0
- * writes zeros.
+ * values under scale bytes 0 to 2 (rounded to a multiple of 2^-133) and for
+ * values of 2^128 and above (e2m1 from byte 253 on, e4m3 from 247), which are
+ * +-Inf as in mx_dequantize_mxfp4, also where their product with x is not.
+ * 0 <= m <= MX_MAX_DECODE_ROWS, 0 <= n <= 2^27 - 16, k % 32 == 0, 0 <= k <=
+ * 2^23, n * k < 2^36, k <= ldx <= 2^28, else MX_ERR_SHAPE; m or n 0 writes
+ * nothing; k 0 writes zeros.
  */
 MX_API mx_status mx_linear_decode(const void* x, int64_t ldx, const uint8_t* qw, const uint8_t* sw, int32_t w_format,
                                   int64_t m, int64_t n, int64_t k, void* c, int32_t c_type, hipStream_t stream);
@@ -148,7 +150,7 @@ MX_API mx_status mx_gated_ffn(const uint8_t* qx, const uint8_t* sx, int32_t x_fo
 
 /*
  * The same of a few bf16 rows (x as for mx_linear_decode): y bf16 (m, cols),
- * 2-byte aligned; cols any.
+ * 2-byte aligned; 0 <= cols <= 2^27 - 16, 2 * cols * k < 2^36.
  */
 MX_API mx_status mx_gated_ffn_decode(const void* x, int64_t ldx, const uint8_t* qw, const uint8_t* sw,
                                      int32_t w_format, int64_t m, int64_t cols, int64_t k, int32_t act, void* y,
