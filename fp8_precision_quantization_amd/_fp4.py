@@ -24,13 +24,21 @@ if _FP4 is not None:
     _CODES[_FP4] = 1
 
 
+def _code_type(t, name):
+    """The format that a dtype says (None: bytes); other numbers are refused."""
+    own = _CODES.get(t.dtype)
+    if own is None and t.dtype.is_floating_point:
+        raise ValueError("%s must hold e4m3 or e2m1 codes or bytes, got %s" % (name, t.dtype))
+    return own
+
+
 def _codes(t, fmt, name, ndim=2):
     """(tensor, format, rows.., k) of an operand's codes; fmt None: by dtype,
     MXFP4 for plain bytes."""
     _gpu(t, name)
     if t.dim() != ndim or not t.is_contiguous() or t.element_size() != 1:
         raise ValueError("%s must be a contiguous one-byte tensor of %d dimensions" % (name, ndim))
-    own = _CODES.get(t.dtype)
+    own = _code_type(t, name)
     if fmt is None:
         f = 1 if own is None else own
     elif fmt in FORMATS:
@@ -45,10 +53,16 @@ def _codes(t, fmt, name, ndim=2):
     return f, k
 
 
+def _scale_type(s, name):
+    if s.dtype.is_floating_point and s.dtype != torch.float8_e8m0fnu:
+        raise ValueError("%s must hold e8m0 scales or bytes, got %s" % (name, s.dtype))
+
+
 def _blocked_scales(s, nbytes, name):
     _gpu(s, name)
     if s.element_size() != 1 or not s.is_contiguous():
         raise ValueError("%s must be a contiguous one-byte tensor" % name)
+    _scale_type(s, name)
     if s.numel() != nbytes:
         raise ValueError("%s: %d bytes of blocked scales expected, got %d" % (name, nbytes, s.numel()))
 
@@ -128,6 +142,7 @@ def mx_dequantize_mxfp4(q, s, blocked: bool = False, out_dtype=torch.bfloat16, o
         _blocked_scales(s, batch * _blocked_numel(rows, cols), "s")
     else:
         _bytes(s, lead + (rows, cols // MX_BLOCK), "s")
+        _scale_type(s, "s")
     _same_device(q.device, s=s)
     code = _out_type(out_dtype)
     x = _new(out, lead + (rows, cols), out_dtype, q.device, "out")
@@ -286,6 +301,9 @@ def mx_gated_ffn_backward(qd, sd, qw, sw, q, s, act: str = "silu", group_end_off
     dev = qd.device
     _bytes(q, (rows, 2 * f), "q")
     _bytes(s, (rows, 2 * f // MX_BLOCK), "s")
+    if _code_type(q, "q"):
+        raise ValueError("q must hold e4m3 codes or bytes, got %s" % q.dtype)
+    _scale_type(s, "s")
     _same_device(dev, q=q, s=s)
     o = _outs(out, 2 if recompute else 1)
     dh = _new(o[0], (rows, 2 * f), torch.bfloat16, dev, "dh")
