@@ -14,7 +14,7 @@ constexpr int64_t kMaxWeights = (int64_t)1 << 36;       // a group's scale offse
 constexpr int64_t kMaxCols = (int64_t)1 << 24;          // and those of 32 rows of a result
 constexpr int64_t kMaxDecodeLd = (int64_t)1 << 28;      // and those of four rows of x
 constexpr int64_t kMaxDecodeCols = 16 * kMaxGridBlocks; // at least 16 columns to a workgroup
-constexpr int64_t kMaxCast = (int64_t)1 << 34;
+constexpr int64_t kMaxCast = (int64_t)1 << 34;         // (below 2^23 workgroups of 256)
 
 bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p % a) == 0; }
 bool type_ok(int32_t t) { return t == MX_TYPE_BF16 || t == MX_TYPE_F32; }

@@ -287,8 +287,6 @@ static int64_t rows_blocks(int64_t batch, int64_t rows, int64_t cols, bool block
   return (batch * pr * pb * 4 + kCast4Threads * runs - 1) / (kCast4Threads * runs);
 }
 
-int64_t cast4_grid_blocks(int64_t batch, int64_t rows, int64_t cols) { return rows_blocks(batch, rows, cols, true, 1); }
-
 hipError_t launch_cast4(const void* x, int64_t batch, int64_t rows, int64_t cols, int64_t ldx, bool f32, uint8_t* q0,
                         uint8_t* s0, uint8_t* q1, uint8_t* s1, bool blocked, hipStream_t stream) {
   Cast4Args a = cast4_args(batch, rows, cols, f32 ? kCast4Cols<float> : kCast4Cols<uint16_t>);

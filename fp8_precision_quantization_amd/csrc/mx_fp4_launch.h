@@ -21,7 +21,6 @@ struct MmOperands {
 // after another; q0/s0 (dim0) and/or q1/s1 (dim1) non-null.
 hipError_t launch_cast4(const void* x, int64_t batch, int64_t rows, int64_t cols, int64_t ldx, bool f32, uint8_t* q0,
                         uint8_t* s0, uint8_t* q1, uint8_t* s1, bool blocked, hipStream_t stream);
-int64_t cast4_grid_blocks(int64_t batch, int64_t rows, int64_t cols);
 hipError_t launch_dequantize4(const uint8_t* q, const uint8_t* s, int64_t batch, int64_t rows, int64_t cols,
                               bool blocked, void* x, bool f32, hipStream_t stream);
 
