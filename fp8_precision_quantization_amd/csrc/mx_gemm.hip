@@ -99,13 +99,6 @@ __device__ __forceinline__ int lds_chunk(int row, int c) {
   return row * kGemmTK + 16 * (c ^ ((row & 7) ^ ((row >> 3) & 1)));
 }
 
-__device__ __forceinline__ int32_t wave_sum(int32_t v) {
-#pragma unroll
-  for (int d = 32; d >= 1; d >>= 1)
-    v += __shfl_xor(v, d);
-  return v;
-}
-
 // Two binary32 values -> their bf16 bits, nearest-even, packed with the
 // first in the low half: gfx950's v_cvt_pk_bf16_f32, one instruction for
 // both.  Checked on MI355X against a software nearest-even rounding over
@@ -247,44 +240,18 @@ __global__ __launch_bounds__(kGemmThreads) void mx_gemm_kernel(GemmArgs a) {
       build_piece_starts(table, a.groups, kGemmTile, a.tiles_n, xs);
     }
     lds_barrier();
-    // Values read from LDS are per-lane to the compiler; readfirstlane
-    // makes them scalar (they are the same in every lane), so that the
-    // buffer descriptors built from them stay in scalar registers.
-    // XCD x's p-th tile: piece p - xs[g] of group g, the last g with
-    // xs[g] <= p (xs[G] = the pieces per XCD in all).
-    const int32_t p = (int32_t)(blockIdx.x / 8), x = (int32_t)(blockIdx.x % 8);
-    if (p >= __builtin_amdgcn_readfirstlane(xs[a.groups]))
+    GroupPiece piece;
+    if (!find_group_piece(table, xs, a.groups, kGemmTile, a.tiles_n, (int32_t)(blockIdx.x / 8),
+                          (int32_t)(blockIdx.x % 8), piece))
       return;  // uniform; no barrier follows
-    int glo = 0, ghi = a.groups;   // xs[glo] <= p < xs[ghi]
-    while (ghi - glo > 1) {
-      const int mid = (glo + ghi) >> 1;
-      if (xs[mid] <= p)
-        glo = mid;
-      else
-        ghi = mid;
-    }
-    const int g = __builtin_amdgcn_readfirstlane(glo);
-    const int32_t lo = __builtin_amdgcn_readfirstlane(table.lo[g]);
-    const int32_t hi = __builtin_amdgcn_readfirstlane(table.hi[g]);
-    const uint32_t trows = (uint32_t)(__builtin_amdgcn_readfirstlane(table.start[g + 1]) -
-                                      __builtin_amdgcn_readfirstlane(table.start[g])) / kGemmTile;
-    const uint32_t tg = trows * a.tiles_n, pg = (tg + 7) / 8;
-    const uint32_t idx = (uint32_t)x * pg + (uint32_t)(p - __builtin_amdgcn_readfirstlane(xs[g]));
-    if (idx >= tg)
-      return;  // uniform; no barrier follows
-    band_tile(idx, trows, tm, tn);
-    const int32_t r0 = lo + (int32_t)tm * kGemmTile;
+    band_tile(piece.tile, piece.tile_rows, tm, tn);
+    const int32_t r0 = piece.lo + (int32_t)tm * kGemmTile;
     row0 = r0;
-    rows_valid = min(kGemmTile, hi - r0);
-    // the tile's first row in A's M-grouped blocked scales: group g starts
-    // there at the sum of the earlier groups' sizes rounded up to 128 rows
-    int32_t part = 0;
-    for (int q = threadIdx.x & 63; q < g; q += 64)
-      part += (table.hi[q] - table.lo[q] + 127) / 128 * 128;
-    srow0 = __builtin_amdgcn_readfirstlane(wave_sum(part)) + (r0 - lo);
+    rows_valid = min(kGemmTile, piece.hi - r0);
+    srow0 = group_scale_row(table, piece.g) + (r0 - piece.lo);   // in A's M-grouped blocked scales
     lds_barrier();   // every wave is done with the tables
-    qb += (int64_t)g * a.n * ld;
-    sb += (int64_t)g * a.sb_bytes;
+    qb += (int64_t)piece.g * a.n * ld;
+    sb += (int64_t)piece.g * a.sb_bytes;
   } else {
     row0 = (int64_t)tm * kGemmTile;
     rows_valid = min((int64_t)kGemmTile, a.m - row0);

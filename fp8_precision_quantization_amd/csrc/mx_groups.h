@@ -156,6 +156,50 @@ __device__ inline void build_piece_starts(const GroupTable& t, int groups, int32
     xs[groups] = total;
 }
 
+// XCD x's p-th tile of a product grouped along M: piece p - xs[g] of group g,
+// the last g with xs[g] <= p (xs[G] = the pieces per XCD in all).  False if there
+// is none (the same in every lane).  Values read from LDS are per-lane to the
+// compiler; readfirstlane makes them scalar, so that the buffer descriptors built
+// from them stay in scalar registers.
+struct GroupPiece {
+  int32_t g, lo, hi;         // the group and its rows
+  uint32_t tile, tile_rows;  // the tile's number in the group, and the group's tile rows
+};
+__device__ __forceinline__ bool find_group_piece(const GroupTable& t, const int32_t* xs, int groups, int32_t unit,
+                                                 uint32_t tiles_n, int32_t p, int32_t x, GroupPiece& out) {
+  if (p >= __builtin_amdgcn_readfirstlane(xs[groups]))
+    return false;
+  int glo = 0, ghi = groups;   // xs[glo] <= p < xs[ghi]
+  while (ghi - glo > 1) {
+    const int mid = (glo + ghi) >> 1;
+    if (xs[mid] <= p)
+      glo = mid;
+    else
+      ghi = mid;
+  }
+  const int g = __builtin_amdgcn_readfirstlane(glo);
+  out.g = g;
+  out.lo = __builtin_amdgcn_readfirstlane(t.lo[g]);
+  out.hi = __builtin_amdgcn_readfirstlane(t.hi[g]);
+  out.tile_rows = (uint32_t)(__builtin_amdgcn_readfirstlane(t.start[g + 1]) -
+                             __builtin_amdgcn_readfirstlane(t.start[g])) / unit;
+  const uint32_t tg = out.tile_rows * tiles_n, pg = (tg + 7) / 8;
+  out.tile = (uint32_t)x * pg + (uint32_t)(p - __builtin_amdgcn_readfirstlane(xs[g]));
+  return out.tile < tg;
+}
+
+// Where group g starts in the M-grouped blocked scales: the earlier groups'
+// sizes, each rounded up to 128 rows.  Every lane of the wave takes part.
+__device__ __forceinline__ int32_t group_scale_row(const GroupTable& t, int g) {
+  int32_t part = 0;
+  for (int h = threadIdx.x & 63; h < g; h += 64)
+    part += (t.hi[h] - t.lo[h] + 127) / 128 * 128;
+#pragma unroll
+  for (int d = 32; d >= 1; d >>= 1)
+    part += __shfl_xor(part, d);
+  return __builtin_amdgcn_readfirstlane(part);
+}
+
 // Starts of the K-grouped blocked scales of row groups: group g covers scale
 // columns (32-row blocks) [lo_g / 32, hi_g / 32) of its clamped row range,
 // padded to a multiple of 4; kstart[g] = sum of the earlier padded widths,

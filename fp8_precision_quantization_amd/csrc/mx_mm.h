@@ -255,38 +255,15 @@ __device__ __forceinline__ bool mm_place(const MmArgs& a, uint8_t* lds, MmPlace&
       build_piece_starts(table, a.groups, TILE, a.tiles_n, xs);
     }
     lds_barrier();
-    if (q >= __builtin_amdgcn_readfirstlane(xs[a.groups]))
+    GroupPiece piece;
+    if (!find_group_piece(table, xs, a.groups, TILE, a.tiles_n, q, x, piece))
       return false;
-    int glo = 0, ghi = a.groups;   // xs[glo] <= q < xs[ghi]
-    while (ghi - glo > 1) {
-      const int mid = (glo + ghi) >> 1;
-      if (xs[mid] <= q)
-        glo = mid;
-      else
-        ghi = mid;
-    }
-    const int g = __builtin_amdgcn_readfirstlane(glo);
-    const int32_t lo = __builtin_amdgcn_readfirstlane(table.lo[g]), hi = __builtin_amdgcn_readfirstlane(table.hi[g]);
-    const uint32_t trows = (uint32_t)(__builtin_amdgcn_readfirstlane(table.start[g + 1]) -
-                                      __builtin_amdgcn_readfirstlane(table.start[g])) / TILE;
-    const uint32_t tg = trows * a.tiles_n, pg = (tg + 7) / 8;
-    const uint32_t idx = (uint32_t)x * pg + (uint32_t)(q - __builtin_amdgcn_readfirstlane(xs[g]));
-    if (idx >= tg)
-      return false;
-    band_tile(idx, trows, tm);
-    const int32_t r0 = lo + (int32_t)tm * TILE;
-    p.group = g;
+    band_tile(piece.tile, piece.tile_rows, tm);
+    const int32_t r0 = piece.lo + (int32_t)tm * TILE;
+    p.group = piece.g;
     p.row0 = r0;
-    p.rows = min(TILE, hi - r0);
-    // group g starts in the scale layout at the earlier groups' sizes, each
-    // rounded up to 128 rows
-    int32_t part = 0;
-    for (int h = threadIdx.x & 63; h < g; h += 64)
-      part += (table.hi[h] - table.lo[h] + 127) / 128 * 128;
-#pragma unroll
-    for (int d = 32; d >= 1; d >>= 1)
-      part += __shfl_xor(part, d);
-    p.srow0 = __builtin_amdgcn_readfirstlane(part) + (r0 - lo);
+    p.rows = min(TILE, piece.hi - r0);
+    p.srow0 = group_scale_row(table, piece.g) + (r0 - piece.lo);
     lds_barrier();   // every wave is done with the table
     return true;
   }
