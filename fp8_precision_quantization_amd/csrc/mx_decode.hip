@@ -212,11 +212,18 @@ __global__ __launch_bounds__(64 * KS) void decode_kernel(DecodeArgs a) {
 
 // Two blocks of 16 rows of W to a workgroup (half the reads of x that one
 // makes), two buffers to a wave, eight waves for up to 16 rows of x and four (or
-// what LDS holds) above: one or two to a SIMD.  Timed (MXFP4, us): 1 x 8192 x
-// 5120 6.7, 3.3 TB/s (one block 8.1, four waves 7.2, four blocks 7.9), 32 x 8192
-// x 5120 9.4 (one block 14.6, three buffers 10.0, seven waves 10.9), 33 x 5120 x
-// 8192 14.7 (one block 25.7, two waves 22, five 14.6), 64 x 5120 x 8192 18.6 (two
-// waves 33): from 33 rows on x is four times the bytes of the workgroup's W.
+// what LDS holds) above: one or two to a SIMD.  Timed (us, best to median): on
+// MXFP4 weights of 8192 x 5120 one row 6.9-7.6 (3.2 TB/s), 16 rows 8.4-8.9, 32 rows
+// 10.8-11.3, 33 rows of 5120 x 8192 15.2-17.0, 64 rows 19.3-21.8; on MXFP8 weights of
+// 8192 x 5120 one row 9.2-9.9 (4.7 TB/s), 16 rows 9.4-10.9, 32 rows 10.6-11.9; gated,
+// 2 x 4096 x 5120: 3 rows 6.8-7.6 and, MXFP8, 9.3-10.0, 33 rows 11.7-13.0 and 11.7-14.0,
+// 64 rows 14.5-16.4.  The choices when they were made: 1 x 8192 x 5120 6.7 (one block
+// 8.1, four waves 7.2, four blocks 7.9), 32 x 8192 x 5120 9.4 (one block 14.6, three
+// buffers 10.0, seven waves 10.9), 33 x 5120 x 8192 14.7 (one block 25.7, two waves
+// 22, five 14.6), 64 x 5120 x 8192 18.6 (two waves 33).  From 33 rows on x is four
+// times the bytes of the workgroup's W, and every workgroup takes all of it: what
+// bounds these is x through LDS, with 96 of 256 CUs idle at 5120 columns.  Cutting K
+// over workgroups would use them, with a workspace for the partial sums.
 template <int FW, int TB, bool GATED>
 static void launch(const DecodeArgs& a, hipStream_t stream) {
   constexpr int RB = GATED ? 1 : 2, kBufs = 2;

@@ -113,8 +113,8 @@ constexpr int kCast4Threads = 256;
 
 // dim0 alone: a lane owns eight columns of a row, a quad a block.  Of bf16 a lane
 // has two of those, whose loads are on their way together (16640 x 5120: 44.0 ->
-// 36.8 us, 5.9 TB/s); of binary32, 32 bytes each, one (66.6 us, 5.8 TB/s; two
-// 69.7).  Blocked scales: the lanes also cover the layout's padding, whose bytes
+// 36.8 us, 5.9 TB/s; 34.7-37.4 on others); of binary32, 32 bytes each, one (66.6 us, 5.8
+// TB/s, two 69.7; 73-76 on others).  Blocked scales: the lanes also cover the layout's padding, whose bytes
 // they clear.
 template <typename T>
 constexpr int kCast4Runs = sizeof(T) == 2 ? 2 : 1;
@@ -160,8 +160,9 @@ __global__ __launch_bounds__(kCast4Threads) void cast4_rows_kernel(Cast4Args a) 
 // so that a block along the rows is 32 / C lanes' and one along the columns two
 // lanes'.  Column codes and all scales leave through LDS: 64 bytes of a column's
 // codes and four scales (a word of the blocked layout) at a time.  16640 x 5120
-// bf16 61 us (4.3 TB/s), 8192 x 5120 binary32 41 (5.2 TB/s; eight columns to a
-// lane took 158 registers, one workgroup to a CU: 62).  Eight waves and 128 bytes
+// bf16 49-53 us (4.9-5.3 TB/s; 61 on a slower card), 8192 x 5120 binary32 38-40
+// (5.3-5.6 TB/s; eight columns to a lane took 158 registers, one workgroup to a CU:
+// 62, where this took 41).  Eight waves and 128 bytes
 // a column are even there and slower on small matrices (2048 x 2048 8.9 -> 9.9
 // us); tiles in pieces per XCD, along rows or columns, gained nothing.
 constexpr int kCast4Waves = 4, kCast4Rows = 32 * kCast4Waves;
@@ -310,7 +311,8 @@ hipError_t launch_cast4(const void* x, int64_t batch, int64_t rows, int64_t cols
 
 // Back: a lane turns eight codes into 16 or 32 bytes.  Every value is a bf16
 // number (or, above byte 252, past its range: Inf).  Bound by memory: 8192 x
-// 5120 to bf16 20 us (5.3 TB/s), 16640 x 5120 33 (6.5 TB/s).
+// 5120 to bf16 19-20 us (5.3-5.6 TB/s), 16640 x 5120 34-39 (5.5-6.3 TB/s), to binary32
+// 82-84 (4.6-4.7 TB/s).
 template <bool F32>
 __global__ __launch_bounds__(kCast4Threads) void dequantize4_kernel(const uint8_t* __restrict__ q, const uint8_t* __restrict__ s,
                                                                     int64_t batch, int64_t rows, int64_t cols,

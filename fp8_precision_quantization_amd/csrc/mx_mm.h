@@ -63,9 +63,15 @@ constexpr int kMmK = 128;     // K of a stage
 // 5632 x 4096 x 4096 62.0 and 60.1; 16 tiles, 6144 x 4096 x 4096 63.1 and 61.3).
 constexpr int kMmSplit = 16;
 // Tile rows to a band of the tile order (the 32 CUs of an XCD then work on 5 x 6
-// tiles or so; us, of 4, 5, 6, 7, 8: block 16640 x 4096 x 5120 in MXFP8 645, 567, 603,
-// 568, 586-633, its gradient 405, 364, 377, 381, 371-377, block 32768 x 2048 x 2048
-// -, 271, 279, 273, 290).
+// tiles or so).  Best of 30 in us, of 5, 7 and 8 (two runs each on one card, without
+// quarters; 4 and 6 lost on the first shape and its gradient): block 16640 x 4096 x
+// 5120 in MXFP8 567-569, 568-572, 586-591, in MXFP4 406-407, 406-408, 425-427, its
+// gradient in MXFP8 364-366, 382-384, 377-379, block 32768 x 2048 x 2048 271-273,
+// 273-275, 290; products in MXFP4: 16640 x 8192 x 5120 373, 377-379, 379-381, 16384
+// x 4096 x 1024 59, 59, 63, 8192 x 4096 x 4096 74, 74, 76; 16 groups of 16640 x 2048
+// x 5120 170-172, 174, 173.  Seven is ahead at 12000 x 5120 x 2048 (block in MXFP4
+// 188-192, 184-185, 184) and 8192 x 4096 x 4096 (block in MXFP8 241-242, 234,
+// 243-246); a launch of small tiles does not show it.
 constexpr int kMmBand = 5;
 
 // Codes of a format: what the MFMA calls it, bytes of a stage's row.
@@ -135,9 +141,10 @@ __device__ __forceinline__ MmRange mm_range(const void* base, uint32_t bytes) {
 // its descriptor by the vector unit (v_readlane, v_readfirstlane: also where the
 // compiler restores a spilled register) by five wait states at the earliest, but
 // one by the scalar unit at once: the block copies the descriptor, which is also
-// what has to stand between the write of m0 and the load.
+// what has to stand between the write of m0 and the load.  (Waiting five states
+// instead cost 1 to 2% of the products and 7% of 33 rows; the copies 0 to 3%.)
 #pragma clang diagnostic push
-#pragma clang diagnostic ignored "-Winline-asm"   // (m0 is reserved, and none of the compiler's own writes of it may move across)
+#pragma clang diagnostic ignored "-Winline-asm"   // (m0 is reserved: no write of it by the compiler may move across)
 template <int BYTES>
 __device__ __forceinline__ void mm_load(uint32_t to, const MmRange& range, uint32_t offset) {
   static_assert(BYTES == 16 || BYTES == 4, "load sizes");
@@ -516,9 +523,15 @@ inline MmArgs mm_args(const MmOperands& in, int64_t m, int64_t n, int64_t w_rows
 
 // Whether a result of m rows and n columns is taken in large tiles: where they
 // nearly fill the GPU.  tile_cols: columns of R that a large tile covers.
-// (Timed, large against small: 256 tiles, 4096 x 4096 x 4096 with MXFP8 rows 52
-// us against 60; 128 tiles, 4096 x 2048 x 2048 25 against 18; 64 tiles, 2048 x
-// 2048 x 4096 in 4 bits 27 against 14.)
+// (Timed, large against small, us: 256 tiles, 4096 x 4096 x 4096 with MXFP8 rows 52
+// against 60; 128 tiles, 4096 x 2048 x 2048 25 against 18; 64 tiles, 2048 x 2048 x
+// 4096 in 4 bits 27 against 14.  Groups are taken as even, and a tile counts whether
+// it is full or not.  16640 rows of 2048 columns: 16 uneven groups, k 5120, 173
+// against 189, in MXFP4 130 against 148; k 2048 in even groups: 32 of 520 rows 88
+// against 88, in 64 of 260 in MXFP4 95 against 98.  It loses where groups end just
+// past a large tile: 16 of 1040 rows 83 against 72, 64 of 260 121 against 112, 16 of
+// 130 rows and 5120 columns 52 against 42; and a block of 4099 x 1056 x 1088 in 4
+// groups takes 18.1 in small tiles where large ones take 16.1 to 17.1.)
 inline bool mm_large(int64_t m, int64_t n, int32_t groups, int tile_cols) {
   const int64_t rows = groups > 1 ? m / groups : m;   // (of a group, if they were even)
   const int64_t tiles = (rows + 255) / 256 * (groups > 1 ? groups : 1) * ((n + tile_cols - 1) / tile_cols);

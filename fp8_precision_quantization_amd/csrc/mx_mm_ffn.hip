@@ -11,18 +11,23 @@
 // Backward: dy = do Wd, whose tile stays in the accumulators; the checkpoint's
 // codes of the same tile come through LDS; dg = dy u act'(g), du = dy act(g).
 //
-// Timed at 16640 rows, 4096 columns, k 5120 (us): block in MXFP8 with the
-// checkpoint 538-590 (2.4-2.6 PFLOP/s), MXFP8 rows and MXFP4 weights 535-560, in
-// MXFP4 383-395; gradient in MXFP8 338-354, in MXFP4 with y again 276-288.
-// Epilogues are 45, 75, 90, 95 and 130 of these: a workgroup has a CU to itself
+// Timed at 16640 rows, 4096 columns, k 5120 (us, best to median): block in MXFP8
+// with the checkpoint 536-621 (2.2-2.6 PFLOP/s), MXFP8 rows and MXFP4 weights
+// 523-571, in MXFP4 380-408; gradient in MXFP8 331-359, MXFP4 weights 306-330, in
+// MXFP4 with y again 270-292.  In 8 uneven groups: block 626-682 and 398-450,
+// gradient 367-410 and 285-320 (a part-filled round and cut tiles to a group).
+// Without their epilogues (copies): block in MXFP8 574 -> 508, in MXFP4 380 -> 313,
+// gradient in MXFP8 334 -> 257, in MXFP4 269 -> 164: a workgroup has a CU to itself
 // (its sums are half of the CU's registers), so nothing covers an epilogue, 300
 // to 540 KB of loads and stores a tile.  Two workgroups of 128 x 128 a CU cover
 // each other's, but load each operand twice as often: 710 for the block, 432 for
 // its gradient in MXFP8, where large tiles took 585 and 376.  Four waves of 128 x
 // 128 to a large tile, as the products take them, leave one wave a SIMD to run
-// the epilogue: 626 and 417 then.  Of the rest, a stage of MXFP8 moves 256 KB
-// through a CU's LDS, 2048 cycles at 128 bytes each, and keeps its MFMAs busy as
-// long.
+// the epilogue: 626 and 417 then.  (Both
+// were timed in MXFP8, with bands of eight tile rows and no quarters; the four
+// waves in MXFP4 too, 503 against 420.)  Of the rest, a stage of MXFP8 moves 256
+// KB through a CU's LDS, 2048 cycles at 128 bytes each, and keeps its MFMAs busy
+// as long.
 #include "mx_gate.h"
 #include "mx_mm_out.h"
 

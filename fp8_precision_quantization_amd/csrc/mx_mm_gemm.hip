@@ -2,13 +2,19 @@
 // MXFP4 or MXFP8, B in MXFP4, dense or grouped along M (mx_mm.h has the
 // product itself).
 //
-// Timed (us): 16640 x 8192 x 5120 in MXFP4, bf16 out, 340-380 (3.7-4.1
-// PFLOP/s; the MFMAs alone, fed the same codes from registers, take 237 and hold
-// the clock at 1.4-1.6 GHz), with MXFP8 rows 489-520 (2.8; the MFMAs alone 3.0);
-// 16640 x 2048 x 5120 in 16 groups with MXFP8 rows 170-187.  Bound by power: the
-// clock is 1.75-1.8 GHz with the MFMAs busy 51% of the cycles, and 2.2 where
-// nothing is loaded.  Large tiles by four waves of 128 x 128 read a third less
-// from LDS than by eight (375 against 360), and here the epilogue is short.
+// Timed (us, best to median): 16640 x 8192 x 5120 in MXFP4, bf16 out, 351-390
+// (3.6-4.0 PFLOP/s), with MXFP8 rows 482-533 (2.6-2.9); 16640 x 2048 x 5120 in 16
+// groups with MXFP8 rows 172-197, in MXFP4 129-138.
+// What the MXFP4 product's 665 thousand cycles go to (copies with a part left
+// out, thousands): its MFMAs are busy 333; without loads, LDS reads and epilogue
+// 429 are left (starts, barriers, scales, the ends of rounds); loads and their
+// waits cost 109 more, LDS reads 26 to 51, the epilogue 80.  So half of the cycles
+// are waits that the one wave of a SIMD has nothing to cover with.  The clock
+// stays at 1.8-1.95 GHz in all of these copies: power sets it, and with it the time
+// of a cycle, not how many there are.  (It also bounds what fewer waits would bring:
+// MFMAs alone and always busy hold the clock at 1.4-1.6 GHz and take 233 us.)
+// Large tiles by four waves of 128 x 128 read a third less from LDS than by eight
+// (375 against 360 us), and here the epilogue is short.
 #include "mx_fp4_launch.h"
 #include "mx_mm_out.h"
 

@@ -48,7 +48,9 @@ struct Staged {
       __builtin_amdgcn_raw_buffer_store_b128(get<u32x4>(row, byte), rs, off, 0, kCacheNT);
     }
   }
-  // The same in elements of E at any alignment, `n` of them a row.
+  // The same in elements of E at any alignment, `n` of them a row.  (16640 x 8191 x
+  // 5120 in MXFP4 443-457 us where 8192 columns take 351-390; 1037 x 1001 x 1056 8.5-9.0
+  // in binary32 and 7.7-8.0 in bf16 where 1000 columns take 7.1-7.7 and 6.8-7.2.)
   template <class E>
   __device__ __forceinline__ void drain_each(E* dst, int64_t ld, int rows, int n) const {
     const int lane = threadIdx.x & 63;
